@@ -1,0 +1,637 @@
+// layer_norm.hip — layer norm forward and backward over the rows of an
+// activation matrix, with the 8-bit form of its input and output.
+//
+//   forward   mu = sum x / C, r = 1 / sqrt(sum (x - mu)^2 / C + eps),
+//             y = (x - mu) r w + b
+//   backward  xh = (x - mu) r, a = dy w,
+//             dx = r (a - mean(a) - xh mean(a xh)),
+//             dw = sum_rows dy xh, db = sum_rows dy
+//
+// All of it is bound by HBM: a row is read once and stays in registers (R
+// chunks of eight columns in each of NT threads), so the forward pass moves
+// 2 e bytes per value and the backward 3 e, or 2 e + 1 when it reads the
+// 8-bit form of x.  Statistics and gradients are fp32; the variance is taken
+// from the centred values in registers, which loses nothing where |mu| is
+// large.  Workgroups stay resident and walk the rows: the weight is read
+// once per workgroup, the next row is on its way while the present one is
+// reduced, and each thread keeps the weight's and bias's gradient of its own
+// columns in registers.  A second launch adds the workgroups' partial sums
+// in a fixed order, so results repeat bit for bit.
+#include "act.hpp"
+
+namespace gq {
+namespace {
+
+
+// Sum over NT threads of A and B at once, in all of them; the order is fixed.
+// red: 2 x 2 x 16 floats, alternated by `phase` so that one barrier suffices.
+template <int NT>
+__device__ __forceinline__ void block_sum2(float& a, float& b, float (*red)[2][16],
+                                           int phase) {
+  a = group_reduce<64>(a, [](float u, float v) { return u + v; });
+  b = group_reduce<64>(b, [](float u, float v) { return u + v; });
+  if constexpr (NT > 64) {
+    const int wave = ((int)threadIdx.x % NT) >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      red[phase][0][wave] = a;
+      red[phase][1][wave] = b;
+    }
+    __syncthreads();
+    a = red[phase][0][0];
+    b = red[phase][1][0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) {
+      a += red[phase][0][i];
+      b += red[phase][1][i];
+    }
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
+  m = lanes_max(m, 64);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) red[((int)threadIdx.x % NT) >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) m = max(m, red[i]);
+    __syncthreads();
+  }
+  return m;
+}
+
+__device__ __forceinline__ void load_vec(const float* __restrict__ p, int c, int cols,
+                                         float none, float (&f)[8]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = none;
+  } else {
+    widen(load8(p + c, cols - c), f);
+  }
+}
+
+// The 8-bit form of a row held as f[R][8]: one step per G lanes, or (G = 0)
+// per row.
+template <typename T, int NT, int R>
+__device__ __forceinline__ void pack_row(const float (&f)[R][8], int lane, int pitch,
+                                         int groups, int G, int8_t* codes,
+                                         float* steps, uint32_t* red) {
+  uint32_t m[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) m[i] = max_abs_bits(f[i]);
+  if (G == 0) {
+    uint32_t t = m[0];
+#pragma unroll
+    for (int i = 1; i < R; ++i) t = max(t, m[i]);
+    t = block_max<NT>(t, red);
+#pragma unroll
+    for (int i = 0; i < R; ++i) m[i] = t;
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) m[i] = lanes_max(m[i], G);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int c = lane + i * NT;
+    const Step s = step_of<T>(m[i]);
+    if (c * 8 < pitch) {
+      *reinterpret_cast<uint2*>(codes + c * 8) = codes8(f[i], s);
+      if (G == 0 ? c == 0 : (c & (G - 1)) == 0 && c / G < groups)
+        steps[G == 0 ? 0 : c / G] = s.step;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- forward --
+// One row per NT threads; a workgroup of BT threads walks BT / NT rows at a
+// time.  xG / yG: lanes per group of the 8-bit form written in the same pass
+// (0: one step per row), where its codes are asked for.
+template <typename T, int NT, int R>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
+    int64_t rows, int cols, int pitch, int groups, int G, LayerNormArgs a) {
+  constexpr int BT = NT < 256 ? 256 : NT;
+  constexpr int PER = BT / NT;
+  __shared__ float red[2][2][16];
+  __shared__ uint32_t redm[16];
+  const int lane = (int)threadIdx.x % NT;
+  const T* x = (const T*)a.x;
+  T* y = (T*)a.y;
+  const int64_t stride = (int64_t)gridDim.x * PER;
+  int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / NT;
+  if (row >= rows) return;  // whole waves; the whole workgroup where PER = 1
+  float w[R][8], b[R][8];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int c = (lane + i * NT) * 8;
+    load_vec(a.weight, c, cols, 1.f, w[i]);
+    load_vec(a.bias, c, cols, 0.f, b[i]);
+  }
+  Raw8<T> raw[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int c = (lane + i * NT) * 8;
+    raw[i] = load8(x + row * a.ldx + c, cols - c);
+  }
+  const float n = (float)cols;
+  int phase = 0;
+  for (;;) {
+    float f[R][8], sum = 0.f, none = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      widen(raw[i], f[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += f[i][j];
+    }
+    const int64_t next = row + stride;
+    if (next < rows) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int c = (lane + i * NT) * 8;
+        raw[i] = load8(x + next * a.ldx + c, cols - c);
+      }
+    }
+    if (a.x_codes)
+      pack_row<T, NT, R>(f, lane, pitch, groups, G, a.x_codes + row * pitch,
+                         a.x_steps + row * groups, redm);
+    block_sum2<NT>(sum, none, red, phase);
+    phase ^= 1;
+    const float mean = sum / n;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (lane + i * NT) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[i][j] -= mean;
+        if (c + j < cols) ss = fmaf(f[i][j], f[i][j], ss);
+      }
+    }
+    block_sum2<NT>(ss, none, red, phase);
+    phase ^= 1;
+    const float rstd = 1.f / sqrtf(ss / n + a.eps);
+    if (lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (lane + i * NT) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
+      const Raw8<T> o = narrow<T>(f[i]);
+      if (y) store8(y + row * a.ldy + c, o, cols - c);
+      if (a.y_codes) {
+        // the form of y as it is stored; columns past the last are 0
+        widen(o, f[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j >= cols) f[i][j] = 0.f;
+      }
+    }
+    if (a.y_codes)
+      pack_row<T, NT, R>(f, lane, pitch, groups, G, a.y_codes + row * pitch,
+                         a.y_steps + row * groups, redm);
+    row = next;
+    if (row >= rows) return;
+  }
+}
+
+// Rows longer than the registers hold: three reads, the last two from L2.
+template <typename T>
+__global__ __launch_bounds__(1024) void k_layer_norm_long(int64_t rows, int cols,
+                                                          LayerNormArgs a) {
+  __shared__ float red[2][2][16];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    float sum = 0.f, none = 0.f, f[8];
+    for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
+      widen(load8(x + c, cols - c), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += f[j];
+    }
+    block_sum2<1024>(sum, none, red, 0);
+    const float mean = sum / (float)cols;
+    float ss = 0.f;
+    for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
+      widen(load8(x + c, cols - c), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols) ss = fmaf(f[j] - mean, f[j] - mean, ss);
+    }
+    block_sum2<1024>(ss, none, red, 1);
+    const float rstd = 1.f / sqrtf(ss / (float)cols + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
+      float w[8], b[8];
+      widen(load8(x + c, cols - c), f);
+      load_vec(a.weight, c, cols, 1.f, w);
+      load_vec(a.bias, c, cols, 0.f, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean) * rstd, w[j], b[j]);
+      store8((T*)a.y + row * a.ldy + c, narrow<T>(f), cols - c);
+    }
+  }
+}
+
+// --------------------------------------------------------------- backward --
+// x from memory or (FORM) from its codes; a chunk of eight columns lies in
+// one group.
+template <typename T, bool FORM>
+struct XChunk;
+template <typename T>
+struct XChunk<T, false> {
+  Raw8<T> raw;
+  __device__ __forceinline__ void load(const LayerNormBackArgs& a, int64_t row, int c,
+                                       int cols, int, int, int) {
+    raw = load8((const T*)a.x + row * a.ldx + c, cols - c);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const { widen(raw, f); }
+};
+template <typename T>
+struct XChunk<T, true> {
+  uint2 w;
+  float step;
+  __device__ __forceinline__ void load(const LayerNormBackArgs& a, int64_t row, int c,
+                                       int cols, int pitch, int groups, int glog) {
+    w = make_uint2(0, 0);
+    step = 0.f;
+    if (c < cols) {
+      w = *reinterpret_cast<const uint2*>(a.codes + row * pitch + c);
+      step = a.steps[row * groups + (c >> glog)];
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const { decode8(w, step, f); }
+};
+
+// Streams of NT threads walk the rows; BT / NT streams share a workgroup and
+// add their gradients in LDS, stream by stream.  Partial sums of workgroup b:
+// ws[b][0][cols] (weight), ws[b][1][cols] (bias).  GRAD = false: dx only.
+template <typename T, int NT, int R, int BT, bool FORM, bool GRAD>
+__global__ __launch_bounds__(BT) void k_layer_norm_backward(
+    int64_t rows, int cols, int pitch, int groups, int glog, LayerNormBackArgs a) {
+  constexpr int S = BT / NT;
+  __shared__ float red_all[S][2][2][16];
+  extern __shared__ float part[];  // S > 1: [NT * R * 8]
+  const int stream = (int)threadIdx.x / NT, lane = (int)threadIdx.x % NT;
+  float(*red)[2][16] = red_all[stream];
+  // every stream of a workgroup takes the same number of turns (barriers)
+  const int64_t stride = (int64_t)gridDim.x * S;
+  const int64_t first = (int64_t)blockIdx.x * S;
+  float w[R][8], gw[R][8], gb[R][8];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    load_vec(a.weight, (lane + i * NT) * 8, cols, 1.f, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[i][j] = gb[i][j] = 0.f;
+  }
+  Raw8<T> rdy[R];
+  XChunk<T, FORM> rx[R];
+  float mean = 0.f, rstd = 0.f;
+  auto fetch = [&](int64_t row) {
+    if (row < rows) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int c = (lane + i * NT) * 8;
+        rdy[i] = load8((const T*)a.dy + row * a.lddy + c, cols - c);
+        rx[i].load(a, row, c, cols, pitch, groups, glog);
+      }
+      mean = a.mean[row];
+      rstd = a.rstd[row];
+    }
+  };
+  fetch(first + stream);
+  const float n = (float)cols;
+  int phase = 0;
+  for (int64_t base = first; base < rows; base += stride) {
+    const int64_t row = base + stream;
+    const bool live = row < rows;
+    float d[R][8], xh[R][8], s1 = 0.f, s2 = 0.f;
+    const float mu = mean, rs = rstd;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (lane + i * NT) * 8;
+      widen(rdy[i], d[i]);
+      rx[i].get(xh[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = live && c + j < cols;
+        xh[i][j] = in ? (xh[i][j] - mu) * rs : 0.f;
+        d[i][j] = in ? d[i][j] : 0.f;
+        if constexpr (GRAD) {
+          gw[i][j] = fmaf(d[i][j], xh[i][j], gw[i][j]);
+          gb[i][j] += d[i][j];
+        }
+        d[i][j] *= w[i][j];
+        s1 += d[i][j];
+        s2 = fmaf(d[i][j], xh[i][j], s2);
+      }
+    }
+    fetch(row + stride);
+    block_sum2<NT>(s1, s2, red, phase);
+    phase ^= 1;
+    const float m1 = s1 / n, m2 = s2 / n;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int c = (lane + i * NT) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[i][j] = rs * (d[i][j] - fmaf(xh[i][j], m2, m1));
+        store8((T*)a.dx + row * a.lddx + c, narrow<T>(d[i]), cols - c);
+      }
+    }
+  }
+  if constexpr (GRAD) {
+    if constexpr (S > 1) {
+      // stream by stream, the weight's sums and then the bias's
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        auto& g = k == 0 ? gw : gb;
+        for (int s = 0; s < S; ++s) {
+          if (stream == s) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const int c = (lane + i * NT) * 8;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                if (s > 0) g[i][j] += part[c + j];
+                if (s < S - 1) part[c + j] = g[i][j];
+              }
+            }
+          }
+          __syncthreads();
+        }
+      }
+    }
+    if (stream == S - 1) {
+      float* o = a.ws + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int c = (lane + i * NT) * 8;
+        Raw8<float> q;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.v[j] = gw[i][j];
+        store8(o + c, q, cols - c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.v[j] = gb[i][j];
+        store8(o + cols + c, q, cols - c);
+      }
+    }
+  }
+}
+
+// Rows longer than the registers hold: dx reads each row twice; the column
+// sums are a pass of their own over strips of 2048 columns.
+template <typename T, bool FORM>
+__global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
+    int64_t rows, int cols, int pitch, int groups, int glog, LayerNormBackArgs a) {
+  __shared__ float red[2][2][16];
+  int phase = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const float mu = a.mean[row], rs = a.rstd[row];
+    float s1 = 0.f, s2 = 0.f, d[8], xh[8], w[8];
+    XChunk<T, FORM> rx;
+    for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
+      widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
+      rx.load(a, row, c, cols, pitch, groups, glog);
+      rx.get(xh);
+      load_vec(a.weight, c, cols, 1.f, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = c + j < cols ? d[j] * w[j] : 0.f;
+        const float h = c + j < cols ? (xh[j] - mu) * rs : 0.f;
+        s1 += v;
+        s2 = fmaf(v, h, s2);
+      }
+    }
+    block_sum2<1024>(s1, s2, red, phase);
+    phase ^= 1;
+    const float m1 = s1 / (float)cols, m2 = s2 / (float)cols;
+    for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
+      widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
+      rx.load(a, row, c, cols, pitch, groups, glog);
+      rx.get(xh);
+      load_vec(a.weight, c, cols, 1.f, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        d[j] = rs * (d[j] * w[j] - fmaf((xh[j] - mu) * rs, m2, m1));
+      store8((T*)a.dx + row * a.lddx + c, narrow<T>(d), cols - c);
+    }
+  }
+}
+
+template <typename T, bool FORM>
+__global__ __launch_bounds__(256) void k_layer_norm_columns(
+    int64_t rows, int cols, int pitch, int groups, int glog, LayerNormBackArgs a) {
+  const int c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8;
+  if (c >= cols) return;
+  float gw[8] = {}, gb[8] = {}, d[8], xh[8];
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const float mu = a.mean[row], rs = a.rstd[row];
+    widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
+    XChunk<T, FORM> rx;
+    rx.load(a, row, c, cols, pitch, groups, glog);
+    rx.get(xh);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      gw[j] = fmaf(d[j], (xh[j] - mu) * rs, gw[j]);
+      gb[j] += d[j];
+    }
+  }
+  float* o = a.ws + (int64_t)blockIdx.y * 2 * cols;
+  store8(o + c, narrow<float>(gw), cols - c);
+  store8(o + cols + c, narrow<float>(gb), cols - c);
+}
+
+// dweight / dbias <- beta * old + the parts' sum.  32 columns by 32 slices of
+// the parts per workgroup; slices are added in order.
+__global__ __launch_bounds__(1024) void k_layer_norm_reduce(
+    int parts, int cols, const float* __restrict__ ws, float beta,
+    float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float sh[32][33];
+  const int col = (int)blockIdx.x * 32 + (int)(threadIdx.x & 31);  // of 2 * cols
+  const int slice = (int)threadIdx.x >> 5;
+  float s = 0.f;
+  if (col < 2 * cols)
+    for (int p = slice; p < parts; p += 32) s += ws[(int64_t)p * 2 * cols + col];
+  sh[slice][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (slice == 0 && col < 2 * cols) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += sh[i][threadIdx.x & 31];
+    float* o = col < cols ? dw : db;
+    if (o) {
+      o += col < cols ? col : col - cols;
+      *o = beta == 0.f ? s : fmaf(beta, *o, s);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- launch --
+// Calls f<NT, R>() for a row of `cols` columns: NT * R * 8 >= cols.
+template <typename F>
+void by_columns(int64_t cols, F f) {
+  if (cols <= 512) f.template operator()<64, 1>();
+  else if (cols <= 1024) f.template operator()<64, 2>();
+  else if (cols <= 2048) f.template operator()<256, 1>();
+  else if (cols <= 4096) f.template operator()<256, 2>();
+  else if (cols <= 8192) f.template operator()<512, 2>();
+  else f.template operator()<1024, 2>();
+}
+constexpr int64_t kLongRow = 16384;
+
+// Whether the rows' 8-bit form is written by the norm's own pass.
+bool fused_form(const ActDims& A) {
+  return A.cols <= kLongRow && (A.whole_row || A.group <= 512);
+}
+
+// Threads of a workgroup of the backward pass.
+template <int NT>
+constexpr int kBackThreads = NT < 512 ? 512 : NT;
+
+// Workgroups of the backward pass: rows are shared out over at most as many
+// threads as the chip holds at the kernel's occupancy.
+int back_streams(const ActDims& A, int nt, int bt) {
+  const int64_t s = bt / nt, need = (A.rows + s - 1) / s;
+  const int64_t most = (int64_t)kCus * (1024 / bt);
+  return (int)(need < most ? need : most);
+}
+
+template <typename T>
+struct Forward {
+  const ActDims& A;
+  const LayerNormArgs& a;
+  hipStream_t st;
+  template <int NT, int R>
+  void operator()() {
+    constexpr int BT = NT < 256 ? 256 : NT, PER = BT / NT;
+    const int64_t need = (A.rows + PER - 1) / PER, most = (int64_t)kCus * (2048 / BT);
+    k_layer_norm<T, NT, R><<<(unsigned)(need < most ? need : most), BT, 0, st>>>(
+        A.rows, (int)A.cols, (int)A.pitch, A.groups, A.whole_row ? 0 : A.group / 8, a);
+  }
+};
+
+template <typename T>
+int forward_t(const ActDims& A, const LayerNormArgs& a, hipStream_t st) {
+  if (A.cols <= kLongRow) {
+    by_columns(A.cols, Forward<T>{A, a, st});
+  } else {
+    k_layer_norm_long<T><<<(unsigned)(A.rows < 512 ? A.rows : 512), 1024, 0, st>>>(
+        A.rows, (int)A.cols, a);
+  }
+  return (int)hipGetLastError();
+}
+
+int glog_of(const ActDims& A) {
+  int g = 31;
+  if (!A.whole_row)
+    for (g = 0; (1 << g) < A.group;) ++g;
+  return g;
+}
+
+template <typename T, bool FORM, bool GRAD>
+struct Backward {
+  const ActDims& A;
+  const LayerNormBackArgs& a;
+  hipStream_t st;
+  int* parts;
+  template <int NT, int R>
+  void operator()() {
+    constexpr int BT = kBackThreads<NT>, S = BT / NT;
+    *parts = back_streams(A, NT, BT);
+    const size_t lds = S > 1 && GRAD ? sizeof(float) * NT * R * 8 : 0;
+    k_layer_norm_backward<T, NT, R, BT, FORM, GRAD><<<(unsigned)*parts, BT, lds, st>>>(
+        A.rows, (int)A.cols, (int)A.pitch, A.groups, glog_of(A), a);
+  }
+};
+
+constexpr int kColumnSlices = 64;
+
+template <typename T, bool FORM>
+int backward_t(const ActDims& A, const LayerNormBackArgs& a, hipStream_t st) {
+  const bool grad = a.dweight || a.dbias;
+  int parts = 0;
+  if (A.rows > 0) {
+    if (A.cols <= kLongRow) {
+      if (grad) by_columns(A.cols, Backward<T, FORM, true>{A, a, st, &parts});
+      else by_columns(A.cols, Backward<T, FORM, false>{A, a, st, &parts});
+    } else {
+      // the column sums first: dx may be written over dy
+      if (grad) {
+        parts = (int)(A.rows < kColumnSlices ? A.rows : kColumnSlices);
+        k_layer_norm_columns<T, FORM>
+            <<<dim3(div_up(A.cols, 2048), parts), 256, 0, st>>>(
+                A.rows, (int)A.cols, (int)A.pitch, A.groups, glog_of(A), a);
+      }
+      k_layer_norm_backward_long<T, FORM>
+          <<<(unsigned)(A.rows < 512 ? A.rows : 512), 1024, 0, st>>>(
+              A.rows, (int)A.cols, (int)A.pitch, A.groups, glog_of(A), a);
+    }
+  }
+  int rc = (int)hipGetLastError();
+  if (rc == 0 && grad) {
+    k_layer_norm_reduce<<<div_up(2 * A.cols, 32), 1024, 0, st>>>(
+        parts, (int)A.cols, a.ws, a.beta, a.dweight, a.dbias);
+    rc = (int)hipGetLastError();
+  }
+  return rc;
+}
+
+struct Parts {
+  const ActDims& A;
+  int* parts;
+  template <int NT, int R>
+  void operator()() { *parts = back_streams(A, NT, kBackThreads<NT>); }
+};
+
+}  // namespace
+
+int launch_layer_norm(const ActDims& A, const LayerNormArgs& in, hipStream_t st) {
+  if (A.rows == 0) return 0;
+  LayerNormArgs a = in;
+  const bool fused = fused_form(A);
+  if (!fused) {
+    // x first: y may be written over it
+    if (a.x_codes) {
+      const int rc = launch_act_pack(A, a.x, a.ldx, a.x_codes, a.x_steps, st);
+      if (rc) return rc;
+    }
+    a.x_codes = a.y_codes = nullptr;
+  }
+  int rc;
+  switch (A.dtype) {
+    case GQ_F32: rc = forward_t<float>(A, a, st); break;
+    case GQ_BF16: rc = forward_t<__bf16>(A, a, st); break;
+    default: rc = forward_t<_Float16>(A, a, st);
+  }
+  if (rc == 0 && !fused && in.y_codes)
+    rc = launch_act_pack(A, a.y, a.ldy, in.y_codes, in.y_steps, st);
+  return rc;
+}
+
+bool layer_norm_needs_y(const ActDims& A) { return !fused_form(A); }
+
+int64_t layer_norm_workspace(const ActDims& A) {
+  int parts = kColumnSlices;
+  if (A.cols <= kLongRow) by_columns(A.cols, Parts{A, &parts});
+  return (int64_t)parts * 2 * A.cols * (int64_t)sizeof(float);
+}
+
+int launch_layer_norm_backward(const ActDims& A, const LayerNormBackArgs& a,
+                               hipStream_t st) {
+  switch (A.dtype) {
+    case GQ_F32:
+      return a.codes ? backward_t<float, true>(A, a, st) : backward_t<float, false>(A, a, st);
+    case GQ_BF16:
+      return a.codes ? backward_t<__bf16, true>(A, a, st)
+                     : backward_t<__bf16, false>(A, a, st);
+    default:
+      return a.codes ? backward_t<_Float16, true>(A, a, st)
+                     : backward_t<_Float16, false>(A, a, st);
+  }
+}
+
+}  // namespace gq

@@ -31,7 +31,14 @@ SYMBOLS = ("gq_code_bits", "gq_payload_size", "gq_select_levels",
            "gq_allocate_layer_bits", "gq_alloc_payload_bytes",
            "gq_quantize_layers_alloc", "gq_dequantize_accumulate_layers_alloc",
            "gq_elias_max_words", "gq_elias_encode", "gq_elias_decode",
+           "gq_act_size", "gq_act_pack", "gq_act_unpack",
+           "gq_act_linear_workspace", "gq_act_linear",
+           "gq_act_wgrad_workspace", "gq_act_wgrad", "gq_layer_norm",
+           "gq_layer_norm_workspace", "gq_layer_norm_backward",
            "gq_strerror", "gq_version")
+
+GQ_F32, GQ_BF16, GQ_F16 = 0, 1, 2
+DTYPES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16, torch.float16: GQ_F16}
 
 
 class gq_desc(C.Structure):
@@ -43,6 +50,15 @@ class gq_desc(C.Structure):
         return (f"gq_desc(scheme={self.scheme}, bucket={self.bucket}, s={self.s}, "
                 f"levels={self.levels}, flags={self.flags}, "
                 f"clip_sigma={self.clip_sigma})")
+
+
+class gq_act(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64),
+                ("dtype", C.c_int32), ("group", C.c_int32)]
+
+    def __repr__(self) -> str:
+        return (f"gq_act(rows={self.rows}, cols={self.cols}, "
+                f"dtype={self.dtype}, group={self.group})")
 
 
 class GQError(RuntimeError):
@@ -86,6 +102,19 @@ def _load():
     lib.gq_elias_max_words.argtypes = [D, i64, C.POINTER(i64)]
     lib.gq_elias_encode.argtypes = [D, i64, P, P, P, P]
     lib.gq_elias_decode.argtypes = [D, i64, P, P, i64, P, P]
+    A, f32 = C.POINTER(gq_act), C.c_float
+    lib.gq_act_size.argtypes = [A, C.POINTER(i64), C.POINTER(i64)]
+    lib.gq_act_pack.argtypes = [A, P, i64, P, P, P]
+    lib.gq_act_unpack.argtypes = [A, P, P, P, i64, P]
+    lib.gq_act_linear_workspace.argtypes = [A, i64, C.POINTER(i64)]
+    lib.gq_act_linear.argtypes = [A, i64, P, P, P, P, P, P, i64, P, i64, P]
+    lib.gq_act_wgrad_workspace.argtypes = [A, i64, C.POINTER(i64)]
+    lib.gq_act_wgrad.argtypes = [A, i64, P, i64, P, P, f32, P, P, P, i64, P]
+    lib.gq_layer_norm.argtypes = [A, P, i64, P, P, f32, P, i64, P, P, P, P, P,
+                                  P, P]
+    lib.gq_layer_norm_workspace.argtypes = [A, C.POINTER(i64)]
+    lib.gq_layer_norm_backward.argtypes = [A, P, i64, P, i64, P, P, P, P, P, P,
+                                           i64, f32, P, P, P, i64, P]
     lib.gq_strerror.argtypes = [C.c_int]
     lib.gq_strerror.restype = C.c_char_p
     lib.gq_version.argtypes = []
@@ -459,3 +488,201 @@ def gq_dequantize_accumulate_layers_alloc(n: int, layer_offsets: torch.Tensor,
         arr(segments, torch.int64, "segments"), alpha, beta,
         _ptr(out, torch.float32, "out"), _stream(stream, out)),
         "gq_dequantize_accumulate_layers_alloc")
+
+
+# ------------------------------------------ 8-bit activations ----
+def act(rows: int, cols: int, dtype: torch.dtype = torch.bfloat16,
+        group: int = 0) -> gq_act:
+    """Descriptor of an activation matrix and its 8-bit form: ``group``
+    columns share a step (a power of two, 32..32768; 0: one step per row)."""
+    if dtype not in DTYPES:
+        raise TypeError(f"act: no activations of type {dtype}")
+    a = gq_act(rows, cols, DTYPES[dtype], group)
+    a.torch_dtype = dtype
+    gq_act_size(a)                  # raises for what the library refuses
+    a.pitch = -(-cols // 16) * 16
+    a.groups = -(-cols // group) if group else 1
+    return a
+
+
+def gq_act_size(a: gq_act):
+    """(bytes of codes, number of steps) of the 8-bit form."""
+    cb, ns = C.c_int64(), C.c_int64()
+    _check(_lib.gq_act_size(C.byref(a), C.byref(cb), C.byref(ns)),
+           "gq_act_size")
+    return cb.value, ns.value
+
+
+def alloc_act(a: gq_act, device="cuda"):
+    """Device buffers of an 8-bit form: (codes int8 [rows, pitch], steps fp32
+    [rows, groups])."""
+    return (torch.empty(a.rows, a.pitch, dtype=torch.int8, device=device),
+            torch.empty(a.rows, a.groups, dtype=torch.float32, device=device))
+
+
+def alloc_workspace(nbytes: int, device="cuda"):
+    """A workspace of that many bytes, or None for 0."""
+    if nbytes == 0:
+        return None
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _matrix(t, dtype, rows: int, cols: int, what: str):
+    """(pointer, row stride) of a device matrix with contiguous columns."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what}: expected shape {(rows, cols)}, got "
+                         f"{tuple(t.shape)}")
+    sr, sc = t.stride()
+    if rows <= 1:
+        sr = max(sr, cols)
+    if (sc != 1 and cols > 1) or sr < cols:
+        raise ValueError(f"{what}: columns must be contiguous and rows must "
+                         "not overlap")
+    return t.data_ptr(), sr
+
+
+def _form(codes, steps, a: gq_act, rows: int, what: str):
+    """Pointers of an 8-bit form of `rows` rows."""
+    pc = _ptr(codes, torch.int8, f"{what} codes")
+    ps = _ptr(steps, torch.float32, f"{what} steps")
+    _need(codes, rows * a.pitch, f"{what} codes")
+    _need(steps, rows * a.groups, f"{what} steps")
+    return pc, ps
+
+
+def _vec(t, n: int, what: str):
+    p = _ptr(t, torch.float32, what)
+    if t is not None:
+        _need(t, n, what)
+    return p
+
+
+def _space(t):
+    return (None, 0) if t is None else (_ptr(t, torch.uint8, "workspace"),
+                                        t.numel())
+
+
+def gq_act_pack(a: gq_act, x: torch.Tensor, codes: torch.Tensor,
+                steps: torch.Tensor, stream=None) -> None:
+    px, ld = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
+    pc, ps = _form(codes, steps, a, a.rows, "x")
+    _check(_lib.gq_act_pack(C.byref(a), px, ld, pc, ps, _stream(stream, x)),
+           "gq_act_pack")
+
+
+def gq_act_unpack(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
+                  x: torch.Tensor, stream=None) -> None:
+    px, ld = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
+    pc, ps = _form(codes, steps, a, a.rows, "x")
+    _check(_lib.gq_act_unpack(C.byref(a), pc, ps, px, ld, _stream(stream, x)),
+           "gq_act_unpack")
+
+
+def gq_act_linear_workspace(a: gq_act, out: int) -> int:
+    b = C.c_int64()
+    _check(_lib.gq_act_linear_workspace(C.byref(a), out, C.byref(b)),
+           "gq_act_linear_workspace")
+    return b.value
+
+
+def gq_act_linear(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
+                  w_codes: torch.Tensor, w_steps: torch.Tensor,
+                  bias: torch.Tensor | None, y: torch.Tensor,
+                  workspace: torch.Tensor | None = None, stream=None) -> None:
+    """y [rows, out] <- the linear layer's product in 8-bit integers; codes
+    and steps are the input's form, w_codes and w_steps the weight's."""
+    if y.dim() != 2:
+        raise ValueError("y: expected a matrix")
+    out = y.shape[1]
+    py, ld = _matrix(y, a.torch_dtype, a.rows, out, "y")
+    pc, ps = _form(codes, steps, a, a.rows, "x")
+    wc, ws = _form(w_codes, w_steps, a, out, "weight")
+    pw, nw = _space(workspace)
+    _check(_lib.gq_act_linear(C.byref(a), out, pc, ps, wc, ws,
+                              _vec(bias, out, "bias"), py, ld, pw, nw,
+                              _stream(stream, y)), "gq_act_linear")
+
+
+def gq_act_wgrad_workspace(a: gq_act, out: int) -> int:
+    b = C.c_int64()
+    _check(_lib.gq_act_wgrad_workspace(C.byref(a), out, C.byref(b)),
+           "gq_act_wgrad_workspace")
+    return b.value
+
+
+def gq_act_wgrad(a: gq_act, dy: torch.Tensor, codes: torch.Tensor,
+                 steps: torch.Tensor, dweight: torch.Tensor,
+                 dbias: torch.Tensor | None = None, beta: float = 0.0,
+                 workspace: torch.Tensor | None = None, stream=None) -> None:
+    """dweight [out * cols] <- beta * dweight + dy^T x^, dbias [out] <- beta *
+    dbias + column sums of dy; dy is [rows, out]."""
+    if dy.dim() != 2:
+        raise ValueError("dy: expected a matrix")
+    out = dy.shape[1]
+    pd, ld = _matrix(dy, a.torch_dtype, a.rows, out, "dy")
+    pc, ps = _form(codes, steps, a, a.rows, "x")
+    if dweight is None:
+        raise TypeError("dweight: expected a torch.Tensor")
+    pw, nw = _space(workspace)
+    _check(_lib.gq_act_wgrad(C.byref(a), out, pd, ld, pc, ps, beta,
+                             _vec(dweight, out * a.cols, "dweight"),
+                             _vec(dbias, out, "dbias"), pw, nw,
+                             _stream(stream, dweight)), "gq_act_wgrad")
+
+
+def gq_layer_norm(a: gq_act, x: torch.Tensor, weight: torch.Tensor | None,
+                  bias: torch.Tensor | None, eps: float,
+                  y: torch.Tensor | None, mean: torch.Tensor | None = None,
+                  rstd: torch.Tensor | None = None, x_form=None, y_form=None,
+                  stream=None) -> None:
+    """y <- layer norm of x's rows.  x_form, y_form: (codes, steps) that
+    receive the 8-bit form of x and of y."""
+    px, ldx = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
+    py, ldy = (None, 0) if y is None else _matrix(y, a.torch_dtype, a.rows,
+                                                  a.cols, "y")
+    xc, xs = (None, None) if x_form is None else _form(*x_form, a, a.rows, "x")
+    yc, ys = (None, None) if y_form is None else _form(*y_form, a, a.rows, "y")
+    _check(_lib.gq_layer_norm(
+        C.byref(a), px, ldx, _vec(weight, a.cols, "weight"),
+        _vec(bias, a.cols, "bias"), eps, py, ldy, _vec(mean, a.rows, "mean"),
+        _vec(rstd, a.rows, "rstd"), xc, xs, yc, ys, _stream(stream, x)),
+        "gq_layer_norm")
+
+
+def gq_layer_norm_workspace(a: gq_act) -> int:
+    b = C.c_int64()
+    _check(_lib.gq_layer_norm_workspace(C.byref(a), C.byref(b)),
+           "gq_layer_norm_workspace")
+    return b.value
+
+
+def gq_layer_norm_backward(a: gq_act, dy: torch.Tensor, x,
+                           mean: torch.Tensor, rstd: torch.Tensor,
+                           weight: torch.Tensor | None, dx: torch.Tensor,
+                           dweight: torch.Tensor | None = None,
+                           dbias: torch.Tensor | None = None,
+                           beta: float = 0.0,
+                           workspace: torch.Tensor | None = None,
+                           stream=None) -> None:
+    """dx <- the input's gradient; dweight, dbias <- beta * old + theirs.  x:
+    the input, or (codes, steps) of its 8-bit form."""
+    pd, ldd = _matrix(dy, a.torch_dtype, a.rows, a.cols, "dy")
+    po, ldo = _matrix(dx, a.torch_dtype, a.rows, a.cols, "dx")
+    px = ldx = pc = ps = None
+    if isinstance(x, torch.Tensor):
+        px, ldx = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
+    else:
+        pc, ps = _form(*x, a, a.rows, "x")
+    pw, nw = _space(workspace)
+    _check(_lib.gq_layer_norm_backward(
+        C.byref(a), pd, ldd, px, ldx or 0, pc, ps,
+        _vec(mean, a.rows, "mean"), _vec(rstd, a.rows, "rstd"),
+        _vec(weight, a.cols, "weight"), po, ldo, beta,
+        _vec(dweight, a.cols, "dweight"), _vec(dbias, a.cols, "dbias"),
+        pw, nw, _stream(stream, dy)), "gq_layer_norm_backward")

@@ -333,6 +333,112 @@ int gq_elias_decode(const gq_desc* desc, int64_t n, const uint64_t* offsets,
                     const uint32_t* words, int64_t n_words, uint8_t* codes,
                     void* stream);
 
+/* -------------------------------------------------------------------------
+ * The 8-bit form of activations, and the operators of a training or serving
+ * step that work on it: the step whose weight gradients are what gq_quantize
+ * takes.  A matrix of activations [rows, cols] (tokens x features) is kept as
+ *   codes   int8 [rows][pitch], pitch = cols rounded up to 16, codes past the
+ *           last column 0
+ *   steps   fp32 [rows][groups]: one per `group` consecutive columns of a row
+ *           (the last group of a row may be short), or one per row
+ * with x^ = code * step.  step = 2^k, the smallest with 127 * step >= the
+ * group's largest |x| (at least 2^-126; at most 2^121, and 2^9 for fp16, where
+ * codes saturate and x^ stays finite); code = x / step rounded to the nearest
+ * integer, ties to even.  An all-zero group has step 0.  A group that holds a
+ * NaN or an infinity has step NaN and codes 0: it decodes as NaN, and its
+ * neighbours are untouched.  With a power of two x^ is exact in bf16 and
+ * fp32, so the operators below round nothing when they read it.
+ *
+ * Conventions of these calls, beyond those at the top: activations are device
+ * pointers with a row stride ld (in elements, ld >= cols; columns are
+ * contiguous) and need only their element's alignment, as do fp32 vectors and
+ * gradients (slices of a flat gradient); codes and workspaces are 16-byte
+ * aligned.  rows = 0 is allowed (row pointers may then be NULL): nothing is
+ * written but gradients, as sums over no rows.  Values that are not finite
+ * go through the arithmetic: they may only show in the rows, columns and
+ * sums that use them.  Buffers that are written overlap no other buffer,
+ * except that the layer norms may write over their input of the same type
+ * and row stride.  Gradients are fp32 and are accumulated as grad <- beta *
+ * grad + sum (beta = 0: write-only).  Sums that are split over workgroups are
+ * joined in a fixed order. */
+typedef enum { GQ_F32 = 0, GQ_BF16 = 1, GQ_F16 = 2 } gq_dtype;
+
+typedef struct {
+  int64_t rows;  /* >= 0                                                     */
+  int64_t cols;  /* 1 .. 2^20; rows * cols <= 2^38                           */
+  int32_t dtype; /* gq_dtype of the activations                              */
+  int32_t group; /* columns per step: a power of two, 32 .. 32768; 0 = one
+                    step per row                                             */
+} gq_act;
+
+/* Sizes of an 8-bit form: bytes of codes (rows * pitch) and number of steps.
+ * Either output may be NULL.  Host-only. */
+int gq_act_size(const gq_act* act, int64_t* code_bytes, int64_t* steps);
+
+/* x -> 8-bit form, and back (x <- x^ in act's type). */
+int gq_act_pack(const gq_act* act, const void* x, int64_t ldx, int8_t* codes,
+                float* steps, void* stream);
+int gq_act_unpack(const gq_act* act, const int8_t* codes, const float* steps,
+                  void* x, int64_t ldx, void* stream);
+
+/* Linear layer in 8-bit integers:
+ *   y[t, o] = (sum_c codes[t, c] * w_codes[o, c]) * steps[t] * w_steps[o]
+ *             + bias[o]
+ * The integer sum is exact; the rest is fp32, rounded once to act's type.
+ * codes, steps: the 8-bit form of the layer's input with one step per row
+ * (GQ_EUNSUPPORTED for act->group != 0 and for cols > 131071).  w_codes,
+ * w_steps: the weight [out, cols] in the same layout, one step per output
+ * feature; these may also come from elsewhere: any codes -128 .. 127 (0 past
+ * the last column) and any fp32 steps.  bias fp32 [out] or NULL.  workspace:
+ * gq_act_linear_workspace bytes (may be NULL if that is 0). */
+int gq_act_linear_workspace(const gq_act* act, int64_t out, int64_t* bytes);
+int gq_act_linear(const gq_act* act, int64_t out, const int8_t* codes,
+                  const float* steps, const int8_t* w_codes,
+                  const float* w_steps, const float* bias, void* y,
+                  int64_t ldy, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/* Gradients of a linear layer whose input is kept in 8 bits:
+ *   dweight[o, c] <- beta * dweight[o, c] + sum_t dy[t, o] * x^[t, c]
+ *   dbias[o]      <- beta * dbias[o]      + sum_t dy[t, o]
+ * dy [rows, out] in act's type (fp32 and fp16 are used in full, not rounded
+ * to bf16).  dweight fp32 [out][cols], contiguous: a slice of the flat
+ * gradient that gq_quantize takes.  dbias may be NULL. */
+int gq_act_wgrad_workspace(const gq_act* act, int64_t out, int64_t* bytes);
+int gq_act_wgrad(const gq_act* act, int64_t out, const void* dy, int64_t lddy,
+                 const int8_t* codes, const float* steps, float beta,
+                 float* dweight, float* dbias, void* workspace,
+                 int64_t workspace_bytes, void* stream);
+
+/* Layer norm over the columns: y = (x - mean) * rstd * weight + bias, rstd =
+ * 1 / sqrt(var + eps), var = sum (x - mean)^2 / cols.  weight, bias fp32
+ * [cols] or NULL (1 and 0).  Optional outputs: mean, rstd fp32 [rows] (what
+ * the backward pass takes); the 8-bit form of x (x_codes, x_steps), to keep
+ * for the backward pass in place of x; the 8-bit form of y as act's type
+ * holds it (y_codes, y_steps), the input of gq_act_linear and gq_act_wgrad.
+ * y may be NULL if its 8-bit form is asked for (GQ_EUNSUPPORTED then for cols
+ * > 16384 and for groups > 512 columns). */
+int gq_layer_norm(const gq_act* act, const void* x, int64_t ldx,
+                  const float* weight, const float* bias, float eps, void* y,
+                  int64_t ldy, float* mean, float* rstd, int8_t* x_codes,
+                  float* x_steps, int8_t* y_codes, float* y_steps,
+                  void* stream);
+
+/* Its backward pass, with xh = (x - mean) * rstd and a = dy * weight:
+ *   dx = rstd * (a - mean(a) - xh * mean(a * xh))
+ *   dweight <- beta * dweight + sum_rows dy * xh
+ *   dbias   <- beta * dbias   + sum_rows dy
+ * x is given either as it is (x, ldx; codes = steps = NULL) or in its 8-bit
+ * form (x = NULL).  dweight and dbias may be NULL. */
+int gq_layer_norm_workspace(const gq_act* act, int64_t* bytes);
+int gq_layer_norm_backward(const gq_act* act, const void* dy, int64_t lddy,
+                           const void* x, int64_t ldx, const int8_t* codes,
+                           const float* steps, const float* mean,
+                           const float* rstd, const float* weight, void* dx,
+                           int64_t lddx, float beta, float* dweight,
+                           float* dbias, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* gq_strerror(int status);
 
