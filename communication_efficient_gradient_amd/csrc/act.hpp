@@ -177,6 +177,27 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t m, int G) {
   return m;
 }
 
+// ------------------------------------------------- global memory to LDS --
+// A range of global memory that reads as zeros past its end (ranges of 4 GiB
+// and more are cut there).  The accesses below are buffer instructions: the
+// bounds are checked by the load itself, and unlike the global form they do
+// not make the compiler drain all LDS reads in flight before it uses one.
+typedef __amdgpu_buffer_rsrc_t BufferRange;
+
+__device__ __forceinline__ BufferRange range_of(const void* base, int64_t bytes) {
+  const uint32_t n = bytes < 0xffffffffll ? (uint32_t)bytes : 0xffffffffu;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
+}
+
+constexpr int kPastEnd = (int)0x80000000;  // an offset no range used here has
+
+// 16 bytes per lane into LDS at `to` (the same in all lanes) + 16 * lane,
+// without passing through registers; `each` differs by lane, `all` does not.
+__device__ __forceinline__ void copy16_to_lds(BufferRange from, int each, int all, void* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      from, (__attribute__((address_space(3))) void*)to, 16, each, all, 0, 0);
+}
+
 constexpr int kCus = 256;  // compute units
 
 __host__ __device__ inline int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }

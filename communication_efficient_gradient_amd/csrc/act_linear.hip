@@ -11,29 +11,21 @@
 namespace gq {
 namespace {
 
-// Sixteen bytes of zeros for lanes past the end of a row.
-__device__ __attribute__((aligned(16))) const int8_t kZeros[16] = {};
-
-#define GQ_LDS __attribute__((address_space(3)))
-#define GQ_GLOBAL __attribute__((address_space(1)))
-
-// 16 bytes per lane from global memory into LDS at base + lane * 16, without
-// passing through registers.
-__device__ __forceinline__ void copy16_to_lds(const void* src, void* base) {
-  __builtin_amdgcn_global_load_lds((const GQ_GLOBAL void*)src, (GQ_LDS void*)base, 16, 0, 0);
-}
-
 template <typename T>
-__device__ __forceinline__ void store_out4(T* y, const float (&f)[4], int valid) {
-  T o[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = (T)f[j];
-  if (valid >= 4) {
-    __builtin_memcpy(y, o, sizeof(o));
+struct Word16 {
+  typedef T V __attribute__((ext_vector_type(16 / sizeof(T))));
+};
+
+// Up to 16 bytes of a row of y, of which `valid` values exist.
+template <typename T, typename V>
+__device__ __forceinline__ void store_piece(T* y, const V& w, int valid) {
+  constexpr int E = 16 / (int)sizeof(T);
+  if (valid >= E) {
+    __builtin_memcpy(y, &w, 16);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < valid) y[j] = o[j];
+    for (int j = 0; j < E; ++j)
+      if (j < valid) y[j] = w[j];
   }
 }
 
@@ -46,47 +38,66 @@ struct LinearArgs {
   int64_t ldy;
   int32_t* ws;
   int splits, per;  // per: 128-byte k-tiles of a split
+  int mtiles, ntiles;
 };
 
+// Tile of a workgroup.  Workgroups go round the eight XCDs in turn; each XCD
+// gets a run of consecutive tiles, taken in columns of up to eight tiles of
+// tokens, so that what its L2 holds is used by many of its workgroups.
+__device__ __forceinline__ void tile_of(int mtiles, int ntiles, int* mt, int* nt) {
+  const int total = mtiles * ntiles, id = (int)blockIdx.x;
+  const int xcd = id % 8, per = total / 8, more = total % 8;
+  const int t = xcd * per + min(xcd, more) + id / 8;
+  const int strip = t / (8 * ntiles), first = strip * 8;
+  const int h = min(8, mtiles - first);
+  const int in = t - first * ntiles;
+  *mt = first + in % h;
+  *nt = in / h;
+}
+
 // A tile of BM tokens by BN outputs per workgroup, WM by WN of it per wave, in
-// k-tiles of 128 codes.  LDS rows are 128 bytes in eight 16-byte chunks, chunk
-// j of row r at place j ^ (r / 2 % 8): sixteen lanes that read one chunk of
+// k-tiles of BK codes.  An LDS row is BK bytes in CH 16-byte chunks, chunk j of
+// row r at place j ^ (r / (16 / CH) % CH): sixteen lanes that read one chunk of
 // sixteen rows then touch every bank once.
-template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_act_linear(LinearArgs a) {
+template <typename T, int BM, int BN, int WM, int WN, int BK>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(LinearArgs a) {
+  constexpr int CH = BK / 16, KK = BK / 32, RPI = 64 / CH;
   constexpr int WAVES = (BM / WM) * (BN / WN);
   constexpr int MT = WM / 32, NTL = WN / 32;
-  __shared__ __attribute__((aligned(16))) int8_t lds[2][(BM + BN) * 128];
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  constexpr int BUF = (BM + BN) * BK;
+  __shared__ __attribute__((aligned(16))) int8_t lds[2 * BUF];
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
-  const int64_t m0 = (int64_t)blockIdx.y * BM;
-  const int n0 = (int)blockIdx.x * BN;
+  int mt, nt;
+  tile_of(a.mtiles, a.ntiles, &mt, &nt);
+  const int64_t m0 = (int64_t)mt * BM;
+  const int n0 = nt * BN;
   const int kt0 = (int)blockIdx.z * a.per;
-  const int nk = min(a.per, div_up(a.pitch, 128) - kt0);
+  const int nk = min(a.per, div_up(a.pitch, BK) - kt0);
 
-  // copies: a wave instruction fills 8 rows
-  constexpr int COPIES = (BM + BN) / 8 / WAVES;
-  const int8_t* src[COPIES];
-  int chunk[COPIES];
+  // copies: a wave instruction fills RPI rows.  Rows past the end lie behind
+  // the buffers' ranges and read as zeros.
+  constexpr int CM = BM / RPI / WAVES, CN = BN / RPI / WAVES;
+  const int cl = lane % CH, rl = lane / CH;
+  const BufferRange bm = range_of(a.codes + m0 * a.pitch, (a.rows - m0) * a.pitch);
+  const BufferRange bn = range_of(a.w_codes + (int64_t)n0 * a.pitch,
+                                  (int64_t)(a.out - n0) * a.pitch);
+  auto fill = [&](int kt, int at) {
+    const int k0 = (kt0 + kt) * BK;
+    // chunks past the pitch (in the last, short k-tile) are zeros too
+    const int left = (a.pitch - k0) / 16;
 #pragma unroll
-  for (int i = 0; i < COPIES; ++i) {
-    const int r = (wave * COPIES + i) * 8 + lane / 8;
-    chunk[i] = (lane % 8) ^ (r / 2 % 8);
-    // rows past the end repeat the last one; what they give is not stored
-    if (r < BM) {
-      const int64_t m = min(m0 + r, a.rows - 1);
-      src[i] = a.codes + m * a.pitch;
-    } else {
-      const int n = min(n0 + r - BM, a.out - 1);
-      src[i] = a.w_codes + (int64_t)n * a.pitch;
+    for (int i = 0; i < CM; ++i) {
+      const int r = (wave * CM + i) * RPI + rl, c = cl ^ (r / (16 / CH) % CH);
+      copy16_to_lds(bm, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
+                    &lds[at + (wave * CM + i) * 1024]);
     }
-  }
-  auto fill = [&](int kt, int buf) {
 #pragma unroll
-    for (int i = 0; i < COPIES; ++i) {
-      const int k = (kt0 + kt) * 128 + chunk[i] * 16;
-      copy16_to_lds(k < a.pitch ? src[i] + k : kZeros,
-                    &lds[buf][(wave * COPIES + i) * 1024]);
+    for (int i = 0; i < CN; ++i) {
+      const int r = (wave * CN + i) * RPI + rl, c = cl ^ (r / (16 / CH) % CH);
+      copy16_to_lds(bn, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
+                    &lds[at + BM * BK + (wave * CN + i) * 1024]);
     }
   };
   i32x16 acc[NTL][MT];
@@ -97,59 +108,122 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void k_act_linear(Linea
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-  auto frag = [&](int buf, int row, int kk) {
-    const int r = row + lane % 32;
-    const int p = (kk * 2 + lane / 32) ^ (r / 2 % 8);
-    return *reinterpret_cast<const i32x4*>(&lds[buf][r * 128 + p * 16]);
+  // The next k-step's fragments (32 rows by 32 codes) are read from LDS between
+  // the present one's products (the scheduling groups); the next k-tile is on
+  // its way into the other buffer.
+  const int fr = lane % 32;
+  int place[KK];
+#pragma unroll
+  for (int kk = 0; kk < KK; ++kk)
+    place[kk] = fr * BK + (((kk * 2 + lane / 32) ^ (fr / (16 / CH) % CH)) << 4);
+  i32x4 fm[2][MT], fn[2][NTL];
+  auto read = [&](int to, int at, int kk) {
+    const int8_t* p = &lds[at + place[kk]];
+#pragma unroll
+    for (int i = 0; i < NTL; ++i)
+      fn[to][i] = *reinterpret_cast<const i32x4*>(p + (BM + wn + i * 32) * BK);
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      fm[to][j] = *reinterpret_cast<const i32x4*>(p + (wm + j * 32) * BK);
   };
-  if (nk > 0) fill(0, 0);
+  fill(0, 0);
   __syncthreads();
+  read(0, 0, 0);
+  int at = 0;
   for (int kt = 0; kt < nk; ++kt) {
-    const int buf = kt & 1;
-    if (kt + 1 < nk) fill(kt + 1, buf ^ 1);
+    if (kt + 1 < nk) fill(kt + 1, at ^ BUF);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      i32x4 fm[MT], fn[NTL];
+    for (int kk = 0; kk < KK; ++kk) {
+      if (kk < KK - 1) {
+        read((kk + 1) & 1, at, kk + 1);
+      } else {
+        __syncthreads();  // the next k-tile is in LDS, this one is read
+        at ^= BUF;
+        read(0, at, 0);
+      }
 #pragma unroll
-      for (int j = 0; j < MT; ++j) fm[j] = frag(buf, wm + j * 32, kk);
+      for (int j = 0; j < MT; ++j)
 #pragma unroll
-      for (int i = 0; i < NTL; ++i) fn[i] = frag(buf, BM + wn + i * 32, kk);
+        for (int i = 0; i < NTL; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fn[kk & 1][i], fm[kk & 1][j],
+                                                           acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int g = 0; g < MT + NTL; ++g) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, MT * NTL - MT - NTL, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // A lane holds, of one token per 32 x 32 tile, four consecutive outputs in
+  // each of the tile's four quarters: eight bytes of bf16, at 32 rows of y.
+  // The wave's results therefore go through its own part of LDS, TOK tokens
+  // at a time, and leave as whole 16-byte pieces of WN-long rows (measured at
+  // 8192 x 8192 x 4096: 321 us with direct stores).
+  if (a.splits == 1) {
+    using V = typename Word16<T>::V;  // 16 bytes of results
+    constexpr int E = 16 / (int)sizeof(T), ROW = WN / E;  // pieces per row
+    constexpr int TOK = 32 * (2 / ((int)sizeof(T) / 2) < MT ? 2 / ((int)sizeof(T) / 2) : MT);
+    static_assert(TOK * WN * (int)sizeof(T) * WAVES <= (int)sizeof(lds), "");
+    __syncthreads();  // all waves have read their last fragments
+    int8_t* mine = lds + wave * (TOK * WN * (int)sizeof(T));
+    const int lo = lane / 32 * 4;
+#pragma unroll
+    for (int j0 = 0; j0 < MT; j0 += TOK / 32) {
+      float s[TOK / 32];
+#pragma unroll
+      for (int jj = 0; jj < TOK / 32; ++jj)
+        s[jj] = a.steps[min(m0 + wm + (j0 + jj) * 32 + fr, a.rows - 1)];
 #pragma unroll
       for (int i = 0; i < NTL; ++i)
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fn[i], fm[j], acc[i][j], 0, 0, 0);
+        for (int q = 0; q < 4; ++q) {
+          const int n = i * 32 + q * 8 + lo;
+          float v[4], b[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int o = min(n0 + wn + n + r, a.out - 1);
+            v[r] = a.w_steps[o];
+            b[r] = a.bias ? a.bias[o] : 0.f;
+          }
+#pragma unroll
+          for (int jj = 0; jj < TOK / 32; ++jj) {
+            const int row = jj * 32 + fr;
+            T o[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              o[r] = (T)((float)acc[i][j0 + jj][q * 4 + r] * s[jj] * v[r] + b[r]);
+            // piece p of row `row` is kept at place p ^ (row % ROW)
+            __builtin_memcpy(
+                mine + (row * ROW + ((n / E) ^ (row % ROW))) * 16 + n % E * (int)sizeof(T), o,
+                sizeof(o));
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < TOK * ROW / 64; ++k) {
+        const int row = (k * 64 + lane) / ROW, p = lane % ROW;
+        const V w = *reinterpret_cast<const V*>(mine + (row * ROW + (p ^ (row % ROW))) * 16);
+        const int64_t m = m0 + wm + j0 * 32 + row;
+        const int n = n0 + wn + p * E;
+        if (m < a.rows) store_piece((T*)a.y + m * a.ldy + n, w, a.out - n);
+      }
     }
-    __syncthreads();
+    return;
   }
-  // a lane holds, of one token, four consecutive outputs in each of four
-  // quarters of a 32 x 32 tile
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
     const int64_t m = m0 + wm + j * 32 + lane % 32;
     if (m >= a.rows) continue;
-    const float s = a.steps[m];
 #pragma unroll
     for (int i = 0; i < NTL; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int n = n0 + wn + i * 32 + q * 8 + lane / 32 * 4;
-        if (n >= a.out) continue;
-        if (a.splits > 1) {
-          int32_t* p = a.ws + ((int64_t)blockIdx.z * a.rows + m) * a.out + n;
+        int32_t* p = a.ws + ((int64_t)blockIdx.z * a.rows + m) * a.out + n;
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < a.out) p[r] = acc[i][j][q * 4 + r];
-        } else {
-          float f[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int o = min(n + r, a.out - 1);
-            f[r] = (float)acc[i][j][q * 4 + r] * s * a.w_steps[o] +
-                   (a.bias ? a.bias[o] : 0.f);
-          }
-          store_out4((T*)a.y + m * a.ldy + n, f, a.out - n);
-        }
+        for (int r = 0; r < 4; ++r)
+          if (n + r < a.out) p[r] = acc[i][j][q * 4 + r];
       }
   }
 }
@@ -171,23 +245,28 @@ __global__ __launch_bounds__(256) void k_act_linear_join(LinearArgs a) {
 
 struct Plan {
   int splits, per;
+  int tile;  // rows and columns of a tile
 };
 
 Plan plan_linear(const ActDims& A, int64_t out) {
   const int kt = div_up(A.pitch, 128);
-  const int64_t tiles = ((A.rows + 127) / 128) * ((out + 127) / 128);
+  Plan p;
+  p.tile = ((A.rows + 255) / 256) * ((out + 255) / 256) >= 128 ? 256 : 128;
+  const int64_t tiles = ((A.rows + p.tile - 1) / p.tile) * ((out + p.tile - 1) / p.tile);
   int splits = tiles >= kCus ? 1 : (int)(kCus / tiles);
   if (splits > kt / 4) splits = kt / 4 > 0 ? kt / 4 : 1;
-  Plan p;
   p.per = div_up(kt, splits);
   p.splits = div_up(kt, p.per);
   return p;
 }
 
 template <typename T>
-int linear_t(const ActDims& A, LinearArgs a, hipStream_t st) {
-  const dim3 g(div_up(a.out, 128), div_up(A.rows, 128), a.splits);
-  k_act_linear<T, 128, 128, 64, 64><<<g, 256, 0, st>>>(a);
+int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
+  a.mtiles = div_up(A.rows, tile);
+  a.ntiles = div_up(a.out, tile);
+  const dim3 g(a.mtiles * a.ntiles, 1, a.splits);
+  if (tile == 256) k_act_linear<T, 256, 256, 128, 64, 128><<<g, 512, 0, st>>>(a);
+  else k_act_linear<T, 128, 128, 64, 64, 128><<<g, 256, 0, st>>>(a);
   int rc = (int)hipGetLastError();
   if (rc == 0 && a.splits > 1) {
     const int64_t b = (A.rows * a.out + 255) / 256;
@@ -212,11 +291,11 @@ int launch_act_linear(const ActDims& A, int64_t out, const int8_t* codes,
   if (A.rows == 0) return 0;
   const Plan p = plan_linear(A, out);
   const LinearArgs a = {A.rows,  (int)out, (int)A.pitch, codes, w_codes,  steps,   w_steps,
-                        bias,    y,        ldy,          (int32_t*)ws, p.splits, p.per};
+                        bias,    y,        ldy,          (int32_t*)ws, p.splits, p.per, 0, 0};
   switch (A.dtype) {
-    case GQ_F32: return linear_t<float>(A, a, st);
-    case GQ_BF16: return linear_t<__bf16>(A, a, st);
-    default: return linear_t<_Float16>(A, a, st);
+    case GQ_F32: return linear_t<float>(A, a, p.tile, st);
+    case GQ_BF16: return linear_t<__bf16>(A, a, p.tile, st);
+    default: return linear_t<_Float16>(A, a, p.tile, st);
   }
 }
 
