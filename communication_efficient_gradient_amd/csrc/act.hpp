@@ -30,6 +30,7 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
@@ -179,13 +180,13 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t m, int G) {
 
 // ------------------------------------------------- global memory to LDS --
 // A range of global memory that reads as zeros past its end (ranges of 4 GiB
-// and more are cut there).  The accesses below are buffer instructions: the
+// and more are cut there; a length below zero is none).  The accesses below are buffer instructions: the
 // bounds are checked by the load itself, and unlike the global form they do
 // not make the compiler drain all LDS reads in flight before it uses one.
 typedef __amdgpu_buffer_rsrc_t BufferRange;
 
 __device__ __forceinline__ BufferRange range_of(const void* base, int64_t bytes) {
-  const uint32_t n = bytes < 0xffffffffll ? (uint32_t)bytes : 0xffffffffu;
+  const uint32_t n = (uint32_t)min(max(bytes, (int64_t)0), (int64_t)0xffffffff);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
 }
 
@@ -193,9 +194,9 @@ constexpr int kPastEnd = (int)0x80000000;  // an offset no range used here has
 
 // 16 bytes per lane into LDS at `to` (the same in all lanes) + 16 * lane,
 // without passing through registers; `each` differs by lane, `all` does not.
-__device__ __forceinline__ void copy16_to_lds(BufferRange from, int each, int all, void* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      from, (__attribute__((address_space(3))) void*)to, 16, each, all, 0, 0);
+__device__ __forceinline__ void copy16_to_lds(
+    BufferRange from, int each, int all, __attribute__((address_space(3))) void* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, to, 16, each, all, 0, 0);
 }
 
 constexpr int kCus = 256;  // compute units

@@ -11,6 +11,8 @@
 namespace gq {
 namespace {
 
+typedef __attribute__((address_space(3))) int8_t* LdsPtr;
+
 template <typename T>
 struct Word16 {
   typedef T V __attribute__((ext_vector_type(16 / sizeof(T))));
@@ -91,13 +93,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
     for (int i = 0; i < CM; ++i) {
       const int r = (wave * CM + i) * RPI + rl, c = cl ^ (r / (16 / CH) % CH);
       copy16_to_lds(bm, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
-                    &lds[at + (wave * CM + i) * 1024]);
+                    (LdsPtr)&lds[at + (wave * CM + i) * 1024]);
     }
 #pragma unroll
     for (int i = 0; i < CN; ++i) {
       const int r = (wave * CN + i) * RPI + rl, c = cl ^ (r / (16 / CH) % CH);
       copy16_to_lds(bn, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
-                    &lds[at + BM * BK + (wave * CN + i) * 1024]);
+                    (LdsPtr)&lds[at + BM * BK + (wave * CN + i) * 1024]);
     }
   };
   i32x16 acc[NTL][MT];

@@ -17,6 +17,7 @@ namespace gq {
 namespace {
 
 #define GQ_LDS __attribute__((address_space(3)))
+typedef GQ_LDS char* LdsPtr;
 
 template <typename T>
 constexpr int kPlanes = 1;
@@ -33,185 +34,370 @@ struct WgradArgs {
   const int8_t* codes;
   const float* steps;
   float beta;
-  float *dw, *db;      // results, or the splits' parts [split][out][cols]
-  float *ws_w, *ws_b;
-  int splits;
-  int64_t per;         // tokens of a split, a multiple of 32
+  float *dw, *db;      // results
+  float *ws_w, *ws_b;  // parts: [split][out][cols], [split][ctiles][out]
+  int splits, otiles, ctiles;
+  int64_t per;         // tokens of a split, a multiple of 64
 };
 
-// Element offset of 16-column chunk `ch` of token row t in a tile of W
-// columns.  Chunks (32 bytes) change places with t so that the sixteen rows
-// one transposing read touches fall on different banks.
+// Byte offset of 32-byte chunk `ch` (16 columns) of token row t in a tile of W
+// columns.  One transposing read takes two neighbouring chunks of rows 0..3
+// and 8..11 (or 4..7 and 12..15); the exclusive or spreads those over all
+// banks.
 template <int W>
 __device__ __forceinline__ int place(int t, int ch) {
-  return t * W + ((ch ^ ((t & 3) | (t >> 1 & 4))) << 4);
+  return t * (W * 2) + ((ch ^ ((t & 3) << 1 | (t >> 3 & 1))) << 5);
 }
 
-// Operand of a 16x16x32 product: column col0 + lane % 16, tokens 8 (lane / 16)
-// + 0..7.  Sixteen lanes fetch four rows of 16 columns and get them
-// transposed.
+// Where a lane's part of a 32-column, 16-token operand lies: column lane % 32,
+// tokens 8 (lane / 32) + 0..3 of a tile that starts at chunk `ch` (even); the
+// next four tokens lie 4 rows further at the same place of their row.
 template <int W>
-__device__ __forceinline__ bf16x8 operand(const short* tile, int ch, int lane) {
-  const int t = lane / 16 * 8 + lane % 16 / 4, part = lane % 4 * 4;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (GQ_LDS s16x4*)(tile + place<W>(t, ch) + part));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (GQ_LDS s16x4*)(tile + place<W>(t + 4, ch) + part));
+__device__ __forceinline__ int operand_place(int ch, int lane) {
+  const int t = lane / 32 * 8 + lane % 16 / 4;
+  return place<W>(t, ch + lane / 16 % 2) + lane % 4 * 8;
+}
+
+template <int W>
+__device__ __forceinline__ bf16x8 operand(LdsPtr p) {
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((GQ_LDS s16x4*)p);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((GQ_LDS s16x4*)(p + 4 * W * 2));
   return __builtin_bit_cast(
       bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_act_wgrad(WgradArgs a) {
-  constexpr int P = kPlanes<T>, BT = 128;
-  __shared__ __attribute__((aligned(16))) short lds_a[P][32 * BT];
-  __shared__ __attribute__((aligned(16))) short lds_b[32 * BT];
-  __shared__ float lds_s[32][BT];
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wo = wave % 2 * 64, wc = wave / 2 * 64;
-  const int o0 = (int)blockIdx.y * BT, c0 = (int)blockIdx.x * BT;
+// Tile of a workgroup: workgroups go round the eight XCDs in turn; each XCD
+// gets a run of consecutive tiles, in columns of up to eight tiles of output
+// features, so that its workgroups share what its L2 holds.
+__device__ __forceinline__ void tile_of(int otiles, int ctiles, int* ot, int* ct) {
+  const int total = otiles * ctiles, id = (int)blockIdx.x;
+  const int xcd = id % 8, per = total / 8, more = total % 8;
+  const int t = xcd * per + min(xcd, more) + id / 8;
+  const int strip = t / (8 * ctiles), first = strip * 8;
+  const int h = min(8, otiles - first);
+  const int in = t - first * ctiles;
+  *ot = first + in % h;
+  *ct = in / h;
+}
+
+// A tile of BO output features by BC columns per workgroup, WO by WC of it per
+// wave, in steps of BK tokens.  While a step's products run, dy of the next
+// step is copied to LDS (COPY: straight from memory, which needs 16-byte
+// rows; otherwise through registers, split into the type's bf16 terms) and
+// its codes, loaded one step earlier, are decoded into LDS.
+template <typename T, bool COPY, int BO, int BC, int WO, int WC, int BK>
+__global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(WgradArgs a) {
+  constexpr int P = kPlanes<T>;
+  static_assert(!COPY || P == 1, "");
+  constexpr int WAVES = (BO / WO) * (BC / WC), TH = WAVES * 64;
+  constexpr int OT = WO / 32, CT = WC / 32, KK = BK / 16;
+  constexpr int ABUF = P * BK * BO * 2, BBUF = BK * BC * 2, BUF = ABUF + BBUF;
+  __shared__ __attribute__((aligned(16))) char lds[2 * BUF];
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wo = wave % (BO / WO) * WO, wc = wave / (BO / WO) * WC;
+  int ot, ct;
+  tile_of(a.otiles, a.ctiles, &ot, &ct);
+  const int o0 = ot * BO, c0 = ct * BC;
   const int64_t t0 = (int64_t)blockIdx.z * a.per;
   const int64_t t1 = min(t0 + a.per, a.rows);
-  const int tr = tid / 8, ch = tid % 8;  // staging: row, 16-column chunk
-  const bool sum_bias = a.db != nullptr && blockIdx.x == 0;
-  float bsum[16] = {};
-  f32x4 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int steps = (int)((t1 - t0 + BK - 1) / BK);
 
-  for (int64_t t = t0; t < t1; t += 32) {
-    const int64_t row = t + tr;
-    const bool live = row < t1;
-    float v[16];
-    {
-      const T* p = (const T*)a.dy + (live ? row : 0) * a.lddy + o0 + ch * 16;
-      const int valid = live ? a.out - o0 - ch * 16 : 0;
-      float f[8];
-      widen(load8(p, valid), f);
+  // ---- dy.  Rows past the last lie behind the range and read as zeros;
+  // columns past the last hold anything, and what they give is not stored.
+  const char* dy = (const char*)((const T*)a.dy + o0);
+  const int64_t row_bytes = a.lddy * (int64_t)sizeof(T);
+  const int64_t dy_end = ((a.rows - 1) * a.lddy + a.out - o0) * (int64_t)sizeof(T);
+  // copies: a wave instruction fills two rows of 256 columns, or four of 128
+  constexpr int AI = BK * BO * 2 / 1024 / WAVES, LPR = BO / 8;  // lanes per row
+  auto copy_dy = [&](int st, LdsPtr to) {
+    const int64_t first = (t0 + (int64_t)st * BK) * row_bytes;
+    const BufferRange r = range_of(dy + first, dy_end - first);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = f[j];
-      widen(load8(p + 8, valid - 8), f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[8 + j] = f[j];
+    for (int i = 0; i < AI; ++i) {
+      const int t = (wave * AI + i) * (64 / LPR) + lane / LPR, p = lane % LPR;
+      // the 16 bytes that belong at place p of row t
+      const int ch = (p / 2) ^ ((t & 3) << 1 | (t >> 3 & 1));
+      copy16_to_lds(r, t * (int)row_bytes + ch * 32 + p % 2 * 16, 0,
+                    to + (wave * AI + i) * 1024);
     }
-    uint4 w = make_uint4(0, 0, 0, 0);
-    float step = 0.f;
-    const int c = c0 + ch * 16;
-    if (live && c < a.pitch) {
-      w = *reinterpret_cast<const uint4*>(a.codes + row * a.pitch + c);
-      step = a.steps[row * a.groups + min(c >> a.glog, a.groups - 1)];
+  };
+  // through registers: pieces of eight columns, BO / 8 per row
+  constexpr int AP = COPY ? 1 : BK * BO / 8 / TH;
+  Raw8<T> ra[AP];
+  auto load_dy = [&](int st, int i) {
+    const int q = i * TH + tid, t = q / LPR, p = q % LPR;
+    const int64_t row = t0 + (int64_t)st * BK + t;
+    const int valid = row < t1 ? a.out - o0 - p * 8 : 0;
+    ra[i] = load8((const T*)dy + (row < t1 ? row : 0) * a.lddy + p * 8, valid);
+  };
+  float bsum[8] = {};
+  auto write_dy = [&](LdsPtr to, bool sum, int i) {
+    const int q = i * TH + tid, t = q / LPR, p = q % LPR;
+    float v[8];
+    widen(ra[i], v);
+    if (sum) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bsum[j] += v[j];
     }
-    __syncthreads();
-    if (sum_bias) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) bsum[j] += v[j];
-    }
+    for (int k = 0; k < P; ++k) {
+      u32x4 h;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      __bf16 h[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 8; j += 2) {
         // the first eight significant bits, exactly; the rest stays in v
-        const uint32_t b = __float_as_uint(v[j]);
-        h[j] = __builtin_bit_cast(__bf16, (uint16_t)(b >> 16));
-        if (p + 1 < P) v[j] -= __uint_as_float(b & 0xffff0000u);
+        const uint32_t x = __float_as_uint(v[j]), y = __float_as_uint(v[j + 1]);
+        h[j / 2] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        if (k + 1 < P) {
+          v[j] -= __uint_as_float(x & 0xffff0000u);
+          v[j + 1] -= __uint_as_float(y & 0xffff0000u);
+        }
       }
-      __builtin_memcpy(&lds_a[p][place<BT>(tr, ch)], h, 32);
+      *(GQ_LDS u32x4*)(to + k * (BK * BO * 2) + place<BO>(t, p / 2) + p % 2 * 16) = h;
     }
-    {
-      float f[16];
-      decode4(w.x, step, f);
-      decode4(w.y, step, f + 4);
-      decode4(w.z, step, f + 8);
-      decode4(w.w, step, f + 12);
-      __bf16 h[16];
+  };
+
+  // ---- codes: pieces of eight columns, BC / 8 per row
+  constexpr int BP = BK * BC / 8 / TH, PPR = BC / 8;
+  uint2 rc[BP];
+  float rs[BP];
+  const int pc = c0 + tid % PPR * 8;  // TH is a multiple of PPR
+  const int grp = min(pc >> a.glog, a.groups - 1);
+  // unconditional: past the last row everything reads as zero
+  auto load_codes = [&](int st, int i) {
+    const int64_t row = t0 + (int64_t)st * BK;
+    const BufferRange c = range_of(a.codes + row * a.pitch, (a.rows - row) * a.pitch);
+    const BufferRange s = range_of(a.steps + row * a.groups, (a.rows - row) * a.groups * 4);
+    const int t = (i * TH + tid) / PPR;
+    const auto w = __builtin_amdgcn_raw_buffer_load_b64(c, t * a.pitch + pc, 0, 0);
+    rc[i] = make_uint2(w[0], w[1]);
+    rs[i] = __uint_as_float(
+        __builtin_amdgcn_raw_buffer_load_b32(s, (t * a.groups + grp) * 4, 0, 0));
+  };
+  auto write_codes = [&](LdsPtr to, int i) {
+    const int t = (i * TH + tid) / PPR, p = tid % PPR;
+    float f[8];
+    decode8(rc[i], rs[i], f);
+    *(GQ_LDS u32x4*)(to + place<BC>(t, p / 2) + p % 2 * 16) =
+        __builtin_bit_cast(u32x4, narrow<__bf16>(f));
+  };
+
+  // The bias's sums are shared out over the tiles of a row: tile ct takes the
+  // steps st with st % ctiles == ct.
+  const bool bias = a.db != nullptr;
+  auto sum_dy = [&](LdsPtr from) {
+    constexpr int N = BK * BO / 8 / TH;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) h[j] = (__bf16)f[j];
-      __builtin_memcpy(&lds_b[place<BT>(tr, ch)], h, 32);
+    for (int i = 0; i < N; ++i) {
+      const int q = i * TH + tid, t = q / LPR, p = q % LPR;
+      const u32x4 u = *(GQ_LDS u32x4*)(from + place<BO>(t, p / 2) + p % 2 * 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bsum[2 * j] += __uint_as_float(u[j] << 16);
+        bsum[2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
+      }
+    }
+  };
+
+  f32x16 acc[OT][CT];
+#pragma unroll
+  for (int i = 0; i < OT; ++i)
+#pragma unroll
+    for (int j = 0; j < CT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  int pa[OT], pb[CT];
+#pragma unroll
+  for (int i = 0; i < OT; ++i) pa[i] = operand_place<BO>((wo + i * 32) / 16, lane);
+#pragma unroll
+  for (int j = 0; j < CT; ++j) pb[j] = operand_place<BC>((wc + j * 32) / 16, lane);
+  bf16x8 fa[2][OT], fb[2][CT];
+  // operands of sub-step k (a 16-token block and a plane of dy)
+  auto read_a = [&](int to, LdsPtr from, int k) {
+    const LdsPtr q = from + k % P * (BK * BO * 2) + k / P * (16 * BO * 2);
+#pragma unroll
+    for (int i = 0; i < OT; ++i) fa[to][i] = operand<BO>(q + pa[i]);
+  };
+  auto read_b = [&](int to, LdsPtr from, int kk) {
+    const LdsPtr q = from + kk * (16 * BC * 2);
+#pragma unroll
+    for (int j = 0; j < CT; ++j) fb[to][j] = operand<BC>(q + pb[j]);
+  };
+
+  int turn = 0;  // st % ctiles
+  // Step st from (now_a, now_b), with step st + 1 prepared in (next_a, next_b)
+  // and the codes of step st + 2 loaded.  All four are restrict: reads and
+  // writes here do not wait for the copies on their way to next_a.  Past the
+  // last step zeros are prepared.
+  auto step = [&](int st, LdsPtr __restrict__ now_a, LdsPtr __restrict__ now_b,
+                  LdsPtr __restrict__ next_a, LdsPtr __restrict__ next_b) {
+    turn = turn + 1 == a.ctiles ? 0 : turn + 1;
+    const bool sum = bias && turn == ct && st + 1 < steps;
+    if constexpr (COPY) copy_dy(st + 1, next_a);
+#pragma unroll
+    for (int k = 0; k < KK * P; ++k) {
+      const int kk = k / P, p = k % P;
+      if (k + 1 < KK * P) {
+        read_a((k + 1) & 1, now_a, k + 1);
+        if (p == P - 1) read_b((kk + 1) & 1, now_b, kk + 1);
+      } else {
+        __syncthreads();  // the next step is in LDS, this one is read
+        if (COPY && sum) sum_dy(next_a);
+        read_a(0, next_a, 0);
+        read_b(0, next_b, 0);
+      }
+      // the pieces are decoded in the first two sub-steps, which leaves the
+      // loads that follow them the rest of the step
+      if (k < 2) {
+        if constexpr (!COPY) {
+#pragma unroll
+          for (int i = k * AP / 2; i < (k + 1) * AP / 2; ++i) {
+            write_dy(next_a, sum, i);
+            load_dy(st + 2, i);
+          }
+        }
+#pragma unroll
+        for (int i = k * BP / 2; i < (k + 1) * BP / 2; ++i) {
+          write_codes(next_b, i);
+          load_codes(st + 2, i);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < OT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[k & 1][i], fb[kk & 1][j],
+                                                             acc[i][j], 0, 0, 0);
+      // reads and decoding between products
+#pragma unroll
+      for (int g = 0; g < OT * CT; ++g) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        if (COPY && k < 2) __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  const LdsPtr a0 = (LdsPtr)lds, b0 = a0 + ABUF, a1 = a0 + BUF, b1 = a1 + ABUF;
+  if (steps > 0) {
+    if constexpr (COPY) copy_dy(0, a0);
+#pragma unroll
+    for (int i = 0; i < BP; ++i) load_codes(0, i);
+    if constexpr (!COPY) {
+#pragma unroll
+      for (int i = 0; i < AP; ++i) load_dy(0, i);
+#pragma unroll
+      for (int i = 0; i < AP; ++i) {
+        write_dy(a0, bias && ct == 0, i);
+        load_dy(1, i);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BP; ++i) {
+      write_codes(b0, i);
+      load_codes(1, i);
     }
     __syncthreads();
-    bf16x8 fb[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) fb[j] = operand<BT>(lds_b, wc / 16 + j, lane);
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8 fa = operand<BT>(lds_a[p], wo / 16 + i, lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa, acc[i][j], 0, 0, 0);
-      }
+    if (COPY && bias && ct == 0) sum_dy(a0);
+    read_a(0, a0, 0);
+    read_b(0, b0, 0);
   }
-  // a lane holds four consecutive columns of one output feature
+  for (int st = 0; st < steps; st += 2) {
+    step(st, a0, b0, a1, b1);
+    if (st + 1 < steps) step(st + 1, a1, b1, a0, b0);
+  }
+  // a lane holds one column of sixteen output features per 32 x 32 tile, so a
+  // store instruction writes two whole 128-byte lines
   const bool parts = a.splits > 1;
   float* dw = parts ? a.ws_w + (int64_t)blockIdx.z * a.out * a.cols : a.dw;
   const float beta = parts ? 0.f : a.beta;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int o = o0 + wo + i * 16 + lane % 16;
-    if (o >= a.out) continue;
+  for (int j = 0; j < CT; ++j) {
+    const int c = c0 + wc + j * 32 + lane % 32;
+    if (c >= a.cols) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + wc + j * 16 + lane / 16 * 4;
-      float* q = dw + (int64_t)o * a.cols + c;
+    for (int i = 0; i < OT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (c + r < a.cols) q[r] = beta == 0.f ? acc[i][j][r] : fmaf(beta, q[r], acc[i][j][r]);
-    }
+      for (int r = 0; r < 16; ++r) {
+        const int o = o0 + wo + i * 32 + r / 4 * 8 + lane / 32 * 4 + r % 4;
+        if (o >= a.out) continue;
+        float* q = dw + (int64_t)o * a.cols + c;
+        *q = beta == 0.f ? acc[i][j][r] : fmaf(beta, *q, acc[i][j][r]);
+      }
   }
-  if (sum_bias) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) lds_s[tr][ch * 16 + j] = bsum[j];
+  if (bias) {
+    // threads of one piece of columns hold sums of different rows
     __syncthreads();
-    const int o = o0 + tid;
-    if (tid < BT && o < a.out) {
+    float* sh = reinterpret_cast<float*>(lds);  // [TH / LPR][BO]
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sh[tid / LPR * BO + tid % LPR * 8 + j] = bsum[j];
+    __syncthreads();
+    const bool one = a.splits == 1 && a.ctiles == 1;
+    for (int o = tid; o < BO && o0 + o < a.out; o += TH) {
       float s = 0.f;
-      for (int t = 0; t < 32; ++t) s += lds_s[t][tid];
-      if (parts) {
-        a.ws_b[(int64_t)blockIdx.z * a.out + o] = s;
+#pragma unroll
+      for (int t = 0; t < TH / LPR; ++t) s += sh[t * BO + o];
+      if (one) {
+        float* q = a.db + o0 + o;
+        *q = a.beta == 0.f ? s : fmaf(a.beta, *q, s);
       } else {
-        a.db[o] = beta == 0.f ? s : fmaf(beta, a.db[o], s);
+        a.ws_b[((int64_t)blockIdx.z * a.ctiles + ct) * a.out + o0 + o] = s;
       }
     }
   }
 }
 
-// Adds the splits' parts, in order.
-__global__ __launch_bounds__(256) void k_act_wgrad_join(int64_t n, int splits, float beta,
-                                                        const float* __restrict__ parts,
-                                                        float* __restrict__ out) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n;
+// Adds the parts of dw (splits of them) and db (splits * ctiles), in order.
+__global__ __launch_bounds__(256) void k_act_wgrad_join(WgradArgs a) {
+  const int64_t n = a.splits > 1 ? (int64_t)a.out * a.cols : 0;
+  const int64_t total = n + (a.db ? a.out : 0);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
-    float s = parts[i];
-    for (int k = 1; k < splits; ++k) s += parts[k * n + i];
-    out[i] = beta == 0.f ? s : fmaf(beta, out[i], s);
+    const bool w = i < n;
+    const float* q = w ? a.ws_w + i : a.ws_b + (i - n);
+    const int64_t stride = w ? n : a.out;
+    const int parts = w ? a.splits : a.splits * a.ctiles;
+    float s = q[0];
+    for (int k = 1; k < parts; ++k) s += q[k * stride];
+    float* o = w ? a.dw + i : a.db + (i - n);
+    *o = a.beta == 0.f ? s : fmaf(a.beta, *o, s);
   }
 }
 
 struct Plan {
-  int splits;
+  int tile, splits, otiles, ctiles;
   int64_t per;
 };
 
 Plan plan_wgrad(const ActDims& A, int64_t out) {
-  const int64_t tiles = ((out + 127) / 128) * ((A.cols + 127) / 128);
-  const int64_t steps = (A.rows + 31) / 32;
-  int64_t splits = tiles >= 2 * kCus ? 1 : 2 * kCus / tiles;
-  if (splits > steps / 8) splits = steps / 8 > 0 ? steps / 8 : 1;
   Plan p;
-  p.per = steps == 0 ? 32 : (steps + splits - 1) / splits * 32;
-  p.splits = steps == 0 ? 1 : div_up(steps * 32, p.per);
+  p.tile = ((out + 255) / 256) * ((A.cols + 255) / 256) >= 128 ? 256 : 128;
+  p.otiles = div_up(out, p.tile);
+  p.ctiles = div_up(A.cols, p.tile);
+  const int64_t tiles = (int64_t)p.otiles * p.ctiles, steps = (A.rows + 63) / 64;
+  const int64_t fill = p.tile == 256 ? kCus : 2 * kCus;
+  int64_t splits = tiles >= fill ? 1 : fill / tiles;
+  if (splits > steps / 4) splits = steps / 4 > 0 ? steps / 4 : 1;
+  p.per = steps == 0 ? 64 : (steps + splits - 1) / splits * 64;
+  p.splits = steps == 0 ? 1 : div_up(steps * 64, p.per);
   return p;
+}
+
+template <typename T, bool COPY, int BK>
+void wgrad_t(const WgradArgs& a, int tile, hipStream_t st) {
+  const dim3 g(a.otiles * a.ctiles, 1, a.splits);
+  if (tile == 256) k_act_wgrad<T, COPY, 256, 256, 128, 64, BK><<<g, 512, 0, st>>>(a);
+  else k_act_wgrad<T, COPY, 128, 128, 64, 64, BK><<<g, 256, 0, st>>>(a);
 }
 
 }  // namespace
 
 int64_t act_wgrad_workspace(const ActDims& A, int64_t out) {
   const Plan p = plan_wgrad(A, out);
-  return p.splits > 1 ? 4 * (int64_t)p.splits * out * (A.cols + 1) : 0;
+  const int64_t w = p.splits > 1 ? (int64_t)p.splits * out * A.cols : 0;
+  const int64_t b = p.splits * p.ctiles > 1 ? (int64_t)p.splits * p.ctiles * out : 0;
+  return 4 * (w + b);
 }
 
 int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy,
@@ -222,23 +408,23 @@ int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy
   if (!A.whole_row)
     for (glog = 0; (1 << glog) < A.group;) ++glog;
   float* w = (float*)ws;
+  const int64_t wn = p.splits > 1 ? (int64_t)p.splits * out * A.cols : 0;
   const WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, glog,
                        dy,     lddy,     codes,       steps,        beta,     dw,
-                       db,     w,        w + (int64_t)p.splits * out * A.cols,
-                       p.splits, p.per};
-  const dim3 g(div_up(A.cols, 128), div_up(out, 128), p.splits);
-  switch (A.dtype) {
-    case GQ_F32: k_act_wgrad<float><<<g, 256, 0, st>>>(a); break;
-    case GQ_BF16: k_act_wgrad<__bf16><<<g, 256, 0, st>>>(a); break;
-    default: k_act_wgrad<_Float16><<<g, 256, 0, st>>>(a);
-  }
+                       db,     w,        w + wn,      p.splits,     p.otiles, p.ctiles,
+                       p.per};
+  // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
+  const bool copy = A.dtype == GQ_BF16 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
+                    lddy < (1 << 23) &&
+                    out % 8 == 0;
+  if (A.dtype == GQ_F32) wgrad_t<float, false, 32>(a, p.tile, st);
+  else if (A.dtype == GQ_F16) wgrad_t<_Float16, false, 32>(a, p.tile, st);
+  else if (copy) wgrad_t<__bf16, true, 64>(a, p.tile, st);
+  else wgrad_t<__bf16, false, 64>(a, p.tile, st);
   int rc = (int)hipGetLastError();
-  if (rc == 0 && p.splits > 1) {
-    const int64_t n = out * A.cols, b = (n + 255) / 256;
-    k_act_wgrad_join<<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(n, p.splits, beta,
-                                                                     a.ws_w, dw);
-    if (db)
-      k_act_wgrad_join<<<div_up(out, 256), 256, 0, st>>>(out, p.splits, beta, a.ws_b, db);
+  if (rc == 0 && (p.splits > 1 || (db && p.splits * p.ctiles > 1))) {
+    const int64_t n = (p.splits > 1 ? out * A.cols : 0) + out, b = (n + 255) / 256;
+    k_act_wgrad_join<<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(a);
     rc = (int)hipGetLastError();
   }
   return rc;
