@@ -245,6 +245,71 @@ __global__ __launch_bounds__(256) void k_act_linear_join(LinearArgs a) {
   }
 }
 
+// Few tokens (up to 16 * MT): the weight is read once, straight into the
+// products' operand layout (16 codes of one output per lane, 16 outputs by 64
+// codes per instruction), and the tokens' codes come from L2.  A workgroup
+// takes 16 outputs; its eight waves take turns of U * 64 codes along the sum
+// and add up in LDS.  One pass over the weight is all there is to wait for:
+// U loads per wave are in flight at once.
+constexpr int kFewWaves = 8;
+
+template <typename T, int MT, int U>
+__global__ __launch_bounds__(kFewWaves * 64) void k_act_linear_few(LinearArgs a) {
+  __shared__ __attribute__((aligned(16))) int32_t sums[kFewWaves][MT][256];
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int n0 = (int)blockIdx.x * 16;
+  const BufferRange w = range_of(a.w_codes + (int64_t)n0 * a.pitch,
+                                 (int64_t)(a.out - n0) * a.pitch);
+  const BufferRange x = range_of(a.codes, a.rows * a.pitch);
+  const int row = lane % 16 * a.pitch, col = lane / 16 * 16;
+  i32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = i32x4{0, 0, 0, 0};
+  for (int k = wave * (U * 64); k < a.pitch; k += kFewWaves * U * 64) {
+    i32x4 fw[U], fx[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // past the pitch lies the next row: those chunks are zeros
+      const int c = k + u * 64 + col;
+      fw[u] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                            w, c < a.pitch ? row + c : kPastEnd, 0, 0));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = k + u * 64 + col;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        fx[u][i] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       x, c < a.pitch ? row + i * 16 * a.pitch + c : kPastEnd, 0, 0));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u], fx[u][i], acc[i], 0, 0, 0);
+  }
+  // a lane holds four consecutive outputs of token lane % 16
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    *reinterpret_cast<i32x4*>(&sums[wave][i][lane % 16 * 16 + lane / 16 * 4]) = acc[i];
+  __syncthreads();
+#pragma unroll
+  for (int e = (int)threadIdx.x; e < MT * 256; e += kFewWaves * 64) {
+    const int64_t m = e / 16;
+    const int n = n0 + e % 16;
+    int32_t s = 0;
+#pragma unroll
+    for (int v = 0; v < kFewWaves; ++v) s += sums[v][e / 256][e % 256];
+    if (m < a.rows && n < a.out)
+      ((T*)a.y)[m * a.ldy + n] =
+          (T)((float)s * a.steps[m] * a.w_steps[n] + (a.bias ? a.bias[n] : 0.f));
+  }
+}
+
+constexpr int kFewRows = 64;
+
 struct Plan {
   int splits, per;
   int tile;  // rows and columns of a tile
@@ -252,7 +317,8 @@ struct Plan {
 
 Plan plan_linear(const ActDims& A, int64_t out) {
   const int kt = div_up(A.pitch, 128);
-  Plan p;
+  Plan p = {1, kt, 0};
+  if (A.rows <= kFewRows) return p;
   p.tile = ((A.rows + 255) / 256) * ((out + 255) / 256) >= 128 ? 256 : 128;
   const int64_t tiles = ((A.rows + p.tile - 1) / p.tile) * ((out + p.tile - 1) / p.tile);
   int splits = tiles >= kCus ? 1 : (int)(kCus / tiles);
@@ -264,6 +330,13 @@ Plan plan_linear(const ActDims& A, int64_t out) {
 
 template <typename T>
 int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
+  if (A.rows <= kFewRows) {
+    const int g = div_up(a.out, 16), t = kFewWaves * 64;
+    if (A.rows <= 16) k_act_linear_few<T, 1, 8><<<g, t, 0, st>>>(a);
+    else if (A.rows <= 32) k_act_linear_few<T, 2, 4><<<g, t, 0, st>>>(a);
+    else k_act_linear_few<T, 4, 4><<<g, t, 0, st>>>(a);
+    return (int)hipGetLastError();
+  }
   a.mtiles = div_up(A.rows, tile);
   a.ntiles = div_up(a.out, tile);
   const dim3 g(a.mtiles * a.ntiles, 1, a.splits);

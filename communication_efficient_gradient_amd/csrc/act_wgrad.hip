@@ -110,17 +110,23 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   const int64_t dy_end = ((a.rows - 1) * a.lddy + a.out - o0) * (int64_t)sizeof(T);
   // copies: a wave instruction fills two rows of 256 columns, or four of 128
   constexpr int AI = BK * BO * 2 / 1024 / WAVES, LPR = BO / 8;  // lanes per row
-  auto copy_dy = [&](int st, LdsPtr to) {
-    const int64_t first = (t0 + (int64_t)st * BK) * row_bytes;
-    const BufferRange r = range_of(dy + first, dy_end - first);
+  int oa[AI];  // a lane's place in the tile, without the step's first row
 #pragma unroll
-    for (int i = 0; i < AI; ++i) {
-      const int t = (wave * AI + i) * (64 / LPR) + lane / LPR, p = lane % LPR;
-      // the 16 bytes that belong at place p of row t
-      const int ch = (p / 2) ^ ((t & 3) << 1 | (t >> 3 & 1));
-      copy16_to_lds(r, t * (int)row_bytes + ch * 32 + p % 2 * 16, 0,
-                    to + (wave * AI + i) * 1024);
-    }
+  for (int i = 0; i < AI; ++i) {
+    const int t = (wave * AI + i) * (64 / LPR) + lane / LPR, p = lane % LPR;
+    // the 16 bytes that belong at place p of row t
+    const int ch = (p / 2) ^ ((t & 3) << 1 | (t >> 3 & 1));
+    oa[i] = t * (int)row_bytes + ch * 32 + p % 2 * 16;
+  }
+  const char* dy_at = dy + t0 * row_bytes;  // of the step that is copied next
+  int64_t dy_left = dy_end - t0 * row_bytes;
+  auto copy_dy = [&](LdsPtr to) {
+    const BufferRange r = range_of(dy_at, dy_left);
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+      copy16_to_lds(r, oa[i], 0, to + (wave * AI + i) * 1024);
+    dy_at += BK * row_bytes;
+    dy_left -= BK * row_bytes;
   };
   // through registers: pieces of eight columns, BO / 8 per row
   constexpr int AP = COPY ? 1 : BK * BO / 8 / TH;
@@ -163,16 +169,26 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   float rs[BP];
   const int pc = c0 + tid % PPR * 8;  // TH is a multiple of PPR
   const int grp = min(pc >> a.glog, a.groups - 1);
-  // unconditional: past the last row everything reads as zero
-  auto load_codes = [&](int st, int i) {
-    const int64_t row = t0 + (int64_t)st * BK;
-    const BufferRange c = range_of(a.codes + row * a.pitch, (a.rows - row) * a.pitch);
-    const BufferRange s = range_of(a.steps + row * a.groups, (a.rows - row) * a.groups * 4);
-    const int t = (i * TH + tid) / PPR;
-    const auto w = __builtin_amdgcn_raw_buffer_load_b64(c, t * a.pitch + pc, 0, 0);
+  // past the last row everything reads as zero
+  const int tc = tid / PPR;  // token of piece 0; TH / PPR tokens between pieces
+  const int ocode = tc * a.pitch + pc, ostep = (tc * a.groups + grp) * 4;
+  const int8_t* c_at = a.codes + t0 * a.pitch;  // of the step loaded next
+  const float* s_at = a.steps + t0 * a.groups;
+  int64_t rows_left = a.rows - t0;
+  BufferRange rng_c, rng_s;
+  auto next_codes = [&] {
+    rng_c = range_of(c_at, rows_left * a.pitch);
+    rng_s = range_of(s_at, rows_left * a.groups * 4);
+    c_at += (int64_t)BK * a.pitch;
+    s_at += (int64_t)BK * a.groups;
+    rows_left -= BK;
+  };
+  auto load_codes = [&](int i) {
+    const auto w = __builtin_amdgcn_raw_buffer_load_b64(rng_c, ocode,
+                                                        i * (TH / PPR) * a.pitch, 0);
     rc[i] = make_uint2(w[0], w[1]);
-    rs[i] = __uint_as_float(
-        __builtin_amdgcn_raw_buffer_load_b32(s, (t * a.groups + grp) * 4, 0, 0));
+    rs[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        rng_s, ostep, i * (TH / PPR) * a.groups * 4, 0));
   };
   auto write_codes = [&](LdsPtr to, int i) {
     const int t = (i * TH + tid) / PPR, p = tid % PPR;
@@ -234,18 +250,19 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
                   LdsPtr __restrict__ next_a, LdsPtr __restrict__ next_b) {
     turn = turn + 1 == a.ctiles ? 0 : turn + 1;
     const bool sum = bias && turn == ct && st + 1 < steps;
-    if constexpr (COPY) copy_dy(st + 1, next_a);
+    if constexpr (COPY) copy_dy(next_a);
+    next_codes();
 #pragma unroll
     for (int k = 0; k < KK * P; ++k) {
       const int kk = k / P, p = k % P;
       if (k + 1 < KK * P) {
-        read_a((k + 1) & 1, now_a, k + 1);
         if (p == P - 1) read_b((kk + 1) & 1, now_b, kk + 1);
+        read_a((k + 1) & 1, now_a, k + 1);
       } else {
         __syncthreads();  // the next step is in LDS, this one is read
         if (COPY && sum) sum_dy(next_a);
-        read_a(0, next_a, 0);
         read_b(0, next_b, 0);
+        read_a(0, next_a, 0);
       }
       // the pieces are decoded in the first two sub-steps, which leaves the
       // loads that follow them the rest of the step
@@ -260,7 +277,7 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
 #pragma unroll
         for (int i = k * BP / 2; i < (k + 1) * BP / 2; ++i) {
           write_codes(next_b, i);
-          load_codes(st + 2, i);
+          load_codes(i);
         }
       }
 #pragma unroll
@@ -281,9 +298,11 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   };
   const LdsPtr a0 = (LdsPtr)lds, b0 = a0 + ABUF, a1 = a0 + BUF, b1 = a1 + ABUF;
   if (steps > 0) {
-    if constexpr (COPY) copy_dy(0, a0);
+    if constexpr (COPY) copy_dy(a0);
+    next_codes();
 #pragma unroll
-    for (int i = 0; i < BP; ++i) load_codes(0, i);
+    for (int i = 0; i < BP; ++i) load_codes(i);
+    next_codes();
     if constexpr (!COPY) {
 #pragma unroll
       for (int i = 0; i < AP; ++i) load_dy(0, i);
@@ -296,17 +315,19 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
 #pragma unroll
     for (int i = 0; i < BP; ++i) {
       write_codes(b0, i);
-      load_codes(1, i);
+      load_codes(i);
     }
     __syncthreads();
     if (COPY && bias && ct == 0) sum_dy(a0);
     read_a(0, a0, 0);
     read_b(0, b0, 0);
   }
-  for (int st = 0; st < steps; st += 2) {
+  int st = 0;
+  for (; st + 1 < steps; st += 2) {
     step(st, a0, b0, a1, b1);
-    if (st + 1 < steps) step(st + 1, a1, b1, a0, b0);
+    step(st + 1, a1, b1, a0, b0);
   }
+  if (st < steps) step(st, a0, b0, a1, b1);
   // a lane holds one column of sixteen output features per 32 x 32 tile, so a
   // store instruction writes two whole 128-byte lines
   const bool parts = a.splits > 1;

@@ -500,6 +500,7 @@ def act(rows: int, cols: int, dtype: torch.dtype = torch.bfloat16,
     a = gq_act(rows, cols, DTYPES[dtype], group)
     a.torch_dtype = dtype
     gq_act_size(a)                  # raises for what the library refuses
+    a.ref = C.byref(a)
     a.pitch = -(-cols // 16) * 16
     a.groups = -(-cols // group) if group else 1
     return a
@@ -527,14 +528,25 @@ def alloc_workspace(nbytes: int, device="cuda"):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _matrix(t, dtype, rows: int, cols: int, what: str):
-    """(pointer, row stride) of a device matrix with contiguous columns."""
+# These calls are short and made many times a step, so what a correct call
+# passes is recognised with few attribute reads; anything else goes on to the
+# check that names the error.
+def _matrix(t, a, cols: int, what: str):
+    """(pointer, row stride) of a device matrix [a.rows, cols] of a's type
+    with contiguous columns."""
+    rows = a.rows
+    try:
+        if (t.dtype is a.torch_dtype and t.is_cuda and t.shape == (rows, cols)
+                and t.is_contiguous()):
+            return t.data_ptr(), cols
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor")
     if t.device.type != "cuda":
         raise ValueError(f"{what}: must be a device tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.dtype != a.torch_dtype:
+        raise TypeError(f"{what}: expected {a.torch_dtype}, got {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{what}: expected shape {(rows, cols)}, got "
                          f"{tuple(t.shape)}")
@@ -547,46 +559,63 @@ def _matrix(t, dtype, rows: int, cols: int, what: str):
     return t.data_ptr(), sr
 
 
-def _form(codes, steps, a: gq_act, rows: int, what: str):
-    """Pointers of an 8-bit form of `rows` rows."""
-    pc = _ptr(codes, torch.int8, f"{what} codes")
-    ps = _ptr(steps, torch.float32, f"{what} steps")
-    _need(codes, rows * a.pitch, f"{what} codes")
-    _need(steps, rows * a.groups, f"{what} steps")
-    return pc, ps
-
-
-def _vec(t, n: int, what: str):
-    p = _ptr(t, torch.float32, what)
-    if t is not None:
-        _need(t, n, what)
+def _buffer(t, dtype, n: int, what: str):
+    """Pointer of a contiguous device tensor of at least n elements."""
+    try:
+        if (t.dtype is dtype and t.is_cuda and t.numel() >= n
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None:
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    p = _ptr(t, dtype, what)
+    _need(t, n, what)
     return p
 
 
+def _form(codes, steps, a: gq_act, rows: int, what: str):
+    """Pointers of an 8-bit form of `rows` rows."""
+    return (_buffer(codes, torch.int8, rows * a.pitch, what + " codes"),
+            _buffer(steps, torch.float32, rows * a.groups, what + " steps"))
+
+
+def _vec(t, n: int, what: str):
+    return None if t is None else _buffer(t, torch.float32, n, what)
+
+
 def _space(t):
-    return (None, 0) if t is None else (_ptr(t, torch.uint8, "workspace"),
-                                        t.numel())
+    if t is None:
+        return None, 0
+    return _buffer(t, torch.uint8, 0, "workspace"), t.numel()
+
+
+def _queue(stream, ref: torch.Tensor):
+    """The raw stream: the one given, or the current one of ref's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(ref.get_device())
+    return _stream(stream, ref)
 
 
 def gq_act_pack(a: gq_act, x: torch.Tensor, codes: torch.Tensor,
                 steps: torch.Tensor, stream=None) -> None:
-    px, ld = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
+    px, ld = _matrix(x, a, a.cols, "x")
     pc, ps = _form(codes, steps, a, a.rows, "x")
-    _check(_lib.gq_act_pack(C.byref(a), px, ld, pc, ps, _stream(stream, x)),
+    _check(_lib.gq_act_pack(a.ref, px, ld, pc, ps, _queue(stream, x)),
            "gq_act_pack")
 
 
 def gq_act_unpack(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
                   x: torch.Tensor, stream=None) -> None:
-    px, ld = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
+    px, ld = _matrix(x, a, a.cols, "x")
     pc, ps = _form(codes, steps, a, a.rows, "x")
-    _check(_lib.gq_act_unpack(C.byref(a), pc, ps, px, ld, _stream(stream, x)),
+    _check(_lib.gq_act_unpack(a.ref, pc, ps, px, ld, _queue(stream, x)),
            "gq_act_unpack")
 
 
 def gq_act_linear_workspace(a: gq_act, out: int) -> int:
     b = C.c_int64()
-    _check(_lib.gq_act_linear_workspace(C.byref(a), out, C.byref(b)),
+    _check(_lib.gq_act_linear_workspace(a.ref, out, C.byref(b)),
            "gq_act_linear_workspace")
     return b.value
 
@@ -600,18 +629,18 @@ def gq_act_linear(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
     if y.dim() != 2:
         raise ValueError("y: expected a matrix")
     out = y.shape[1]
-    py, ld = _matrix(y, a.torch_dtype, a.rows, out, "y")
+    py, ld = _matrix(y, a, out, "y")
     pc, ps = _form(codes, steps, a, a.rows, "x")
     wc, ws = _form(w_codes, w_steps, a, out, "weight")
     pw, nw = _space(workspace)
-    _check(_lib.gq_act_linear(C.byref(a), out, pc, ps, wc, ws,
+    _check(_lib.gq_act_linear(a.ref, out, pc, ps, wc, ws,
                               _vec(bias, out, "bias"), py, ld, pw, nw,
-                              _stream(stream, y)), "gq_act_linear")
+                              _queue(stream, y)), "gq_act_linear")
 
 
 def gq_act_wgrad_workspace(a: gq_act, out: int) -> int:
     b = C.c_int64()
-    _check(_lib.gq_act_wgrad_workspace(C.byref(a), out, C.byref(b)),
+    _check(_lib.gq_act_wgrad_workspace(a.ref, out, C.byref(b)),
            "gq_act_wgrad_workspace")
     return b.value
 
@@ -625,15 +654,14 @@ def gq_act_wgrad(a: gq_act, dy: torch.Tensor, codes: torch.Tensor,
     if dy.dim() != 2:
         raise ValueError("dy: expected a matrix")
     out = dy.shape[1]
-    pd, ld = _matrix(dy, a.torch_dtype, a.rows, out, "dy")
+    pd, ld = _matrix(dy, a, out, "dy")
     pc, ps = _form(codes, steps, a, a.rows, "x")
-    if dweight is None:
-        raise TypeError("dweight: expected a torch.Tensor")
     pw, nw = _space(workspace)
-    _check(_lib.gq_act_wgrad(C.byref(a), out, pd, ld, pc, ps, beta,
-                             _vec(dweight, out * a.cols, "dweight"),
+    _check(_lib.gq_act_wgrad(a.ref, out, pd, ld, pc, ps, beta,
+                             _buffer(dweight, torch.float32, out * a.cols,
+                                     "dweight"),
                              _vec(dbias, out, "dbias"), pw, nw,
-                             _stream(stream, dweight)), "gq_act_wgrad")
+                             _queue(stream, dweight)), "gq_act_wgrad")
 
 
 def gq_layer_norm(a: gq_act, x: torch.Tensor, weight: torch.Tensor | None,
@@ -643,21 +671,20 @@ def gq_layer_norm(a: gq_act, x: torch.Tensor, weight: torch.Tensor | None,
                   stream=None) -> None:
     """y <- layer norm of x's rows.  x_form, y_form: (codes, steps) that
     receive the 8-bit form of x and of y."""
-    px, ldx = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
-    py, ldy = (None, 0) if y is None else _matrix(y, a.torch_dtype, a.rows,
-                                                  a.cols, "y")
+    px, ldx = _matrix(x, a, a.cols, "x")
+    py, ldy = (None, 0) if y is None else _matrix(y, a, a.cols, "y")
     xc, xs = (None, None) if x_form is None else _form(*x_form, a, a.rows, "x")
     yc, ys = (None, None) if y_form is None else _form(*y_form, a, a.rows, "y")
     _check(_lib.gq_layer_norm(
-        C.byref(a), px, ldx, _vec(weight, a.cols, "weight"),
+        a.ref, px, ldx, _vec(weight, a.cols, "weight"),
         _vec(bias, a.cols, "bias"), eps, py, ldy, _vec(mean, a.rows, "mean"),
-        _vec(rstd, a.rows, "rstd"), xc, xs, yc, ys, _stream(stream, x)),
+        _vec(rstd, a.rows, "rstd"), xc, xs, yc, ys, _queue(stream, x)),
         "gq_layer_norm")
 
 
 def gq_layer_norm_workspace(a: gq_act) -> int:
     b = C.c_int64()
-    _check(_lib.gq_layer_norm_workspace(C.byref(a), C.byref(b)),
+    _check(_lib.gq_layer_norm_workspace(a.ref, C.byref(b)),
            "gq_layer_norm_workspace")
     return b.value
 
@@ -672,17 +699,17 @@ def gq_layer_norm_backward(a: gq_act, dy: torch.Tensor, x,
                            stream=None) -> None:
     """dx <- the input's gradient; dweight, dbias <- beta * old + theirs.  x:
     the input, or (codes, steps) of its 8-bit form."""
-    pd, ldd = _matrix(dy, a.torch_dtype, a.rows, a.cols, "dy")
-    po, ldo = _matrix(dx, a.torch_dtype, a.rows, a.cols, "dx")
+    pd, ldd = _matrix(dy, a, a.cols, "dy")
+    po, ldo = _matrix(dx, a, a.cols, "dx")
     px = ldx = pc = ps = None
     if isinstance(x, torch.Tensor):
-        px, ldx = _matrix(x, a.torch_dtype, a.rows, a.cols, "x")
+        px, ldx = _matrix(x, a, a.cols, "x")
     else:
         pc, ps = _form(*x, a, a.rows, "x")
     pw, nw = _space(workspace)
     _check(_lib.gq_layer_norm_backward(
-        C.byref(a), pd, ldd, px, ldx or 0, pc, ps,
+        a.ref, pd, ldd, px, ldx or 0, pc, ps,
         _vec(mean, a.rows, "mean"), _vec(rstd, a.rows, "rstd"),
         _vec(weight, a.cols, "weight"), po, ldo, beta,
         _vec(dweight, a.cols, "dweight"), _vec(dbias, a.cols, "dbias"),
-        pw, nw, _stream(stream, dy)), "gq_layer_norm_backward")
+        pw, nw, _queue(stream, dy)), "gq_layer_norm_backward")
