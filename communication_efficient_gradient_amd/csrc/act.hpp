@@ -67,6 +67,23 @@ __device__ __forceinline__ void store8(T* __restrict__ p, const Raw8<T>& r, int 
   }
 }
 
+// A chunk that is a row's or past its end as a whole unless RAGGED (cols % 8 !=
+// 0): without the way through single elements the loads of several chunks
+// stay together (pack of 16384 x 4096 bf16: 57 us with it, %s without).
+template <bool RAGGED, typename T>
+__device__ __forceinline__ Raw8<T> load_chunk(const T* p, int valid) {
+  if (RAGGED) return load8(p, valid);
+  Raw8<T> r = {};
+  if (valid > 0) __builtin_memcpy(&r, p, sizeof(r));
+  return r;
+}
+
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void store_chunk(T* p, const Raw8<T>& r, int valid) {
+  if (RAGGED) return store8(p, r, valid);
+  if (valid > 0) __builtin_memcpy(p, &r, sizeof(r));
+}
+
 template <typename T>
 __device__ __forceinline__ void widen(const Raw8<T>& r, float (&f)[8]) {
 #pragma unroll

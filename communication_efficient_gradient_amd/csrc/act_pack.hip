@@ -12,29 +12,59 @@ namespace {
 
 constexpr int kBlock = 256;
 
-// Groups of G * 8 columns, G = 4..64 lanes.  tpr threads per row (a power of
-// two); cpr: chunks of a row rounded up to whole groups.
-template <typename T>
+// A unit is what a workgroup takes at once: kBlock / tpr rows by tpr chunks
+// (tpr a power of two, `turns` units side by side cover the rows).  Each
+// workgroup takes UNITS consecutive ones, all loads first.
+constexpr int UNITS = 2;
+
+struct Unit {
+  int64_t rows0;  // row group
+  int turn;
+};
+
+__device__ __forceinline__ Unit first_unit(int turns) {
+  const int64_t u = (int64_t)blockIdx.x * UNITS;
+  Unit r;
+  // 32-bit division where it is enough: one per workgroup
+  r.rows0 = u >> 32 ? u / turns : (uint32_t)u / (uint32_t)turns;
+  r.turn = (int)(u - r.rows0 * turns);
+  return r;
+}
+
+__device__ __forceinline__ void next_unit(Unit* u, int turns) {
+  if (++u->turn == turns) {
+    u->turn = 0;
+    ++u->rows0;
+  }
+}
+
+// Groups of G * 8 columns, G = 4..64 lanes.
+template <typename T, bool RAGGED>
 __global__ __launch_bounds__(kBlock) void k_act_pack_lanes(
-    int64_t rows, int cols, int pitch, int groups, int G, int cpr, int tpr,
+    int64_t rows, int cols, int pitch, int groups, int Glog, int turns, int tlog,
     const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
     float* __restrict__ steps) {
-  const int per = kBlock / tpr, lane = (int)threadIdx.x & (tpr - 1);
-  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows;
-       r0 += (int64_t)gridDim.x * per) {
-    const int64_t row = r0 + (int)threadIdx.x / tpr;
-    const bool live = row < rows;
-    const T* xr = x + (live ? row : 0) * ldx;
-    for (int c0 = 0; c0 < cpr; c0 += tpr) {
-      const int c = c0 + lane;
-      const int valid = live ? cols - c * 8 : 0;
-      float f[8];
-      widen(load8(xr + c * 8, valid), f);
-      const Step s = step_of<T>(lanes_max(max_abs_bits(f), G));
-      if (!live) continue;
+  const int tpr = 1 << tlog, per = kBlock >> tlog, G = 1 << Glog;
+  const int lane = (int)threadIdx.x & (tpr - 1), in = (int)threadIdx.x >> tlog;
+  Raw8<T> raw[UNITS];
+  Unit u = first_unit(turns), v = u;
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i, next_unit(&u, turns)) {
+    const int64_t row = u.rows0 * per + in;
+    const int c = (u.turn * tpr + lane) * 8;
+    raw[i] = load_chunk<RAGGED>(x + row * ldx + c, row < rows ? cols - c : 0);
+  }
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i, next_unit(&v, turns)) {
+    const int64_t row = v.rows0 * per + in;
+    const int c = v.turn * tpr + lane;
+    float f[8];
+    widen(raw[i], f);
+    const Step s = step_of<T>(lanes_max(max_abs_bits(f), G));
+    if (row < rows) {
       if (c * 8 < pitch)
         *reinterpret_cast<uint2*>(codes + row * pitch + c * 8) = codes8(f, s);
-      const int grp = c / G;
+      const int grp = c >> Glog;
       if ((c & (G - 1)) == 0 && grp < groups) steps[row * groups + grp] = s.step;
     }
   }
@@ -56,7 +86,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
 
 // One group (a whole row, or 1024 columns and more) per NT threads: R chunks
 // of each thread stay in registers; R = 0 reads the group twice.
-template <typename T, int NT, int R>
+template <typename T, int NT, int R, bool RAGGED>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
     int64_t rows, int cols, int pitch, int groups, int group,
     const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
@@ -65,34 +95,45 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
   constexpr int BT = NT < 256 ? 256 : NT;
   constexpr int PER = BT / NT;
   const int lane = (int)threadIdx.x % NT;
-  const int64_t total = rows * groups;
-  for (int64_t s0 = (int64_t)blockIdx.x * PER + threadIdx.x / NT; s0 < total;
-       s0 += (int64_t)gridDim.x * PER) {
-    const int64_t row = groups == 1 ? s0 : s0 / groups;
-    const int grp = (int)(s0 - row * groups);
+  const int64_t total = rows * groups, stride = (int64_t)gridDim.x * PER;
+  int64_t at = (int64_t)blockIdx.x * PER + threadIdx.x / NT;
+  Raw8<T> raw[R > 0 ? R : 1];
+  auto fetch = [&](int64_t s) {
+    const int64_t row = groups == 1 ? s : s / groups;
+    const int lo = (int)(s - row * groups) * group, n = min(group, cols - lo);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int c = (lane + i * NT) * 8;
+      raw[i] = load_chunk<RAGGED>(x + row * ldx + lo + c, s < total ? n - c : 0);
+    }
+  };
+  if constexpr (R > 0) fetch(at);
+  for (; at < total; at += stride) {
+    const int64_t row = groups == 1 ? at : at / groups;
+    const int grp = (int)(at - row * groups);
     const int lo = grp * group;
     const int n = min(group, cols - lo);  // columns of this group
     // codes up to the pitch belong to the row's last group
     const int cn = grp == groups - 1 ? pitch - lo : n;
-    const T* xr = x + row * ldx + lo;
     int8_t* cr = codes + row * pitch + lo;
     uint32_t m = 0;
     if constexpr (R > 0) {
       float f[R][8];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int c = (lane + i * NT) * 8;
-        widen(load8(xr + c, n - c), f[i]);
+        widen(raw[i], f[i]);
         m = max(m, max_abs_bits(f[i]));
       }
+      fetch(at + stride);
       const Step s = step_of<T>(block_max<NT>(m, red));
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
         if (c < cn) *reinterpret_cast<uint2*>(cr + c) = codes8(f[i], s);
       }
-      if (lane == 0) steps[s0] = s.step;
+      if (lane == 0) steps[at] = s.step;
     } else {
+      const T* xr = x + row * ldx + lo;
       float f[8];
       for (int c = lane * 8; c < n; c += NT * 8) {
         widen(load8(xr + c, n - c), f);
@@ -103,49 +144,83 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
         widen(load8(xr + c, n - c), f);
         *reinterpret_cast<uint2*>(cr + c) = codes8(f, s);
       }
-      if (lane == 0) steps[s0] = s.step;
+      if (lane == 0) steps[at] = s.step;
     }
   }
 }
 
-template <typename T>
+template <typename T, bool RAGGED>
 __global__ __launch_bounds__(kBlock) void k_act_unpack(
-    int64_t rows, int cols, int pitch, int groups, int glog, int tpr,
+    int64_t rows, int cols, int pitch, int groups, int glog, int turns, int tlog,
     const int8_t* __restrict__ codes, const float* __restrict__ steps,
     T* __restrict__ x, int64_t ldx) {
-  const int per = kBlock / tpr, lane = (int)threadIdx.x & (tpr - 1);
-  for (int64_t row = (int64_t)blockIdx.x * per + (int)threadIdx.x / tpr; row < rows;
-       row += (int64_t)gridDim.x * per) {
-    const int8_t* cr = codes + row * pitch;
-    const float* sr = steps + row * groups;
-    T* xr = x + row * ldx;
-    for (int c = lane * 8; c < cols; c += tpr * 8) {
-      const uint2 w = *reinterpret_cast<const uint2*>(cr + c);
-      float f[8];
-      decode8(w, sr[c >> glog], f);
-      store8(xr + c, narrow<T>(f), cols - c);
+  const int tpr = 1 << tlog, per = kBlock >> tlog;
+  const int lane = (int)threadIdx.x & (tpr - 1), in = (int)threadIdx.x >> tlog;
+  uint2 w[UNITS];
+  float s[UNITS];
+  Unit u = first_unit(turns), v = u;
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i, next_unit(&u, turns)) {
+    const int64_t row = u.rows0 * per + in;
+    const int c = (u.turn * tpr + lane) * 8;
+    w[i] = make_uint2(0, 0);
+    s[i] = 0.f;
+    if (row < rows && c < cols) {
+      w[i] = *reinterpret_cast<const uint2*>(codes + row * pitch + c);
+      s[i] = steps[row * groups + (c >> glog)];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i, next_unit(&v, turns)) {
+    const int64_t row = v.rows0 * per + in;
+    const int c = (v.turn * tpr + lane) * 8;
+    float f[8];
+    decode8(w[i], s[i], f);
+    store_chunk<RAGGED>(x + row * ldx + c, narrow<T>(f), row < rows ? cols - c : 0);
   }
 }
 
-int pow2_up(int v) {
-  int p = 1;
-  while (p < v) p *= 2;
+int log2_up(int v) {
+  int p = 0;
+  while ((1 << p) < v) ++p;
   return p;
 }
 
-// Workgroups over `n` items of which each takes `per`: enough to fill the
-// chip many times, the rest by stride.
-unsigned blocks_for(int64_t n, int per) {
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / kBlock - 1;
+
+// Rows and chunks of a unit-wise kernel: chunks per row -> threads per row,
+// units side by side, workgroups (0: too many for one launch).
+struct Cover {
+  int tlog, turns;
+  unsigned blocks;
+};
+
+Cover cover(int64_t rows, int chunks) {
+  Cover c;
+  c.tlog = log2_up(chunks < kBlock ? chunks : kBlock);
+  c.turns = div_up(chunks, 1 << c.tlog);
+  const int64_t per = kBlock >> c.tlog, units = (rows + per - 1) / per * c.turns;
+  const int64_t blocks = (units + UNITS - 1) / UNITS;
+  c.blocks = blocks <= kMaxBlocks ? (unsigned)blocks : 0;
+  return c;
+}
+
+// Workgroups over `n` items of which each takes `per` at a time, the rest by
+// stride.
+unsigned blocks_for(int64_t n, int per, int most) {
   const int64_t b = (n + per - 1) / per;
-  return (unsigned)(b < (1 << 20) ? b : (1 << 20));
+  return (unsigned)(b < most ? b : most);
 }
 
 template <typename T, int NT, int R>
 void pack_seg(const ActDims& A, const T* x, int64_t ldx, int8_t* codes,
               float* steps, hipStream_t st) {
   constexpr int BT = NT < 256 ? 256 : NT;
-  k_act_pack_seg<T, NT, R><<<blocks_for(A.rows * A.groups, BT / NT), BT, 0, st>>>(
+  // resident workgroups, each thread with the next group on its way
+  const unsigned g = blocks_for(A.rows * A.groups, BT / NT, kCus * (2048 / BT));
+  auto* k = A.cols % 8 ? k_act_pack_seg<T, NT, R, true> : k_act_pack_seg<T, NT, R, false>;
+  k<<<g, BT, 0, st>>>(
       A.rows, (int)A.cols, (int)A.pitch, A.groups, A.group, x, ldx, codes, steps);
 }
 
@@ -154,10 +229,12 @@ int pack_t(const ActDims& A, const T* x, int64_t ldx, int8_t* codes, float* step
            hipStream_t st) {
   if (!A.whole_row && A.group <= 512) {
     const int G = A.group / 8;
-    const int cpr = div_up(div_up(A.cols, 8), G) * G;
-    const int tpr = cpr < kBlock ? pow2_up(cpr) : kBlock;
-    k_act_pack_lanes<T><<<blocks_for(A.rows, kBlock / tpr), kBlock, 0, st>>>(
-        A.rows, (int)A.cols, (int)A.pitch, A.groups, G, cpr, tpr, x, ldx, codes,
+    // whole groups in each unit
+    const Cover c = cover(A.rows, div_up(div_up(A.cols, 8), G) * G);
+    if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
+    auto* k = A.cols % 8 ? k_act_pack_lanes<T, true> : k_act_pack_lanes<T, false>;
+    k<<<c.blocks, kBlock, 0, st>>>(
+        A.rows, (int)A.cols, (int)A.pitch, A.groups, log2_up(G), c.turns, c.tlog, x, ldx, codes,
         steps);
   } else {
     // pitch, not cols: padding codes are written by the group's threads too
@@ -176,13 +253,14 @@ int pack_t(const ActDims& A, const T* x, int64_t ldx, int8_t* codes, float* step
 template <typename T>
 int unpack_t(const ActDims& A, const int8_t* codes, const float* steps, T* x,
              int64_t ldx, hipStream_t st) {
-  const int n8 = div_up(A.cols, 8);
-  const int tpr = n8 < kBlock ? pow2_up(n8) : kBlock;
+  const Cover c = cover(A.rows, div_up(A.cols, 8));
+  if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
   int glog = 31;  // one step per row: index 0
-  if (!A.whole_row)
-    for (glog = 0; (1 << glog) < A.group;) ++glog;
-  k_act_unpack<T><<<blocks_for(A.rows, kBlock / tpr), kBlock, 0, st>>>(
-      A.rows, (int)A.cols, (int)A.pitch, A.groups, glog, tpr, codes, steps, x, ldx);
+  if (!A.whole_row) glog = log2_up(A.group);
+  auto* k = A.cols % 8 ? k_act_unpack<T, true> : k_act_unpack<T, false>;
+  k<<<c.blocks, kBlock, 0, st>>>(
+      A.rows, (int)A.cols, (int)A.pitch, A.groups, glog, c.turns, c.tlog, codes, steps, x,
+      ldx);
   return (int)hipGetLastError();
 }
 

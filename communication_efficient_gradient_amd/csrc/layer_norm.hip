@@ -70,12 +70,13 @@ __device__ __forceinline__ void load_vec(const float* __restrict__ p, int c, int
   }
 }
 
-// The 8-bit form of a row held as f[R][8]: one step per G lanes, or (G = 0)
-// per row.
+// The 8-bit form of a row held as f[R][8]: one step per 2^Glog lanes, or (Glog
+// < 0) per row.  A chunk below the pitch lies in one of the row's groups.
 template <typename T, int NT, int R>
 __device__ __forceinline__ void pack_row(const float (&f)[R][8], int lane, int pitch,
-                                         int groups, int G, int8_t* codes,
+                                         int groups, int Glog, int8_t* codes,
                                          float* steps, uint32_t* red) {
+  const int G = Glog < 0 ? 0 : 1 << Glog;
   uint32_t m[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) m[i] = max_abs_bits(f[i]);
@@ -96,19 +97,20 @@ __device__ __forceinline__ void pack_row(const float (&f)[R][8], int lane, int p
     const Step s = step_of<T>(m[i]);
     if (c * 8 < pitch) {
       *reinterpret_cast<uint2*>(codes + c * 8) = codes8(f[i], s);
-      if (G == 0 ? c == 0 : (c & (G - 1)) == 0 && c / G < groups)
-        steps[G == 0 ? 0 : c / G] = s.step;
+      if (G == 0 ? c == 0 : (c & (G - 1)) == 0) steps[G == 0 ? 0 : c >> Glog] = s.step;
     }
   }
 }
 
 // ---------------------------------------------------------------- forward --
 // One row per NT threads; a workgroup of BT threads walks BT / NT rows at a
-// time.  xG / yG: lanes per group of the 8-bit form written in the same pass
-// (0: one step per row), where its codes are asked for.
-template <typename T, int NT, int R>
+// time.  2^Glog lanes share a step of the 8-bit forms written in the same pass
+// (Glog < 0: the row does).
+// RAGGED: the last chunk of a row may be short (cols % 8 != 0); otherwise a
+// chunk is a row's or past its end as a whole.
+template <typename T, int NT, int R, bool RAGGED>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
-    int64_t rows, int cols, int pitch, int groups, int G, LayerNormArgs a) {
+    int64_t rows, int cols, int pitch, int groups, int Glog, LayerNormArgs a) {
   constexpr int BT = NT < 256 ? 256 : NT;
   constexpr int PER = BT / NT;
   __shared__ float red[2][2][16];
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int c = (lane + i * NT) * 8;
-    raw[i] = load8(x + row * a.ldx + c, cols - c);
+    raw[i] = load_chunk<RAGGED>(x + row * a.ldx + c, cols - c);
   }
   const float n = (float)cols;
   int phase = 0;
@@ -147,11 +149,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
-        raw[i] = load8(x + next * a.ldx + c, cols - c);
+        raw[i] = load_chunk<RAGGED>(x + next * a.ldx + c, cols - c);
       }
     }
     if (a.x_codes)
-      pack_row<T, NT, R>(f, lane, pitch, groups, G, a.x_codes + row * pitch,
+      pack_row<T, NT, R>(f, lane, pitch, groups, Glog, a.x_codes + row * pitch,
                          a.x_steps + row * groups, redm);
     block_sum2<NT>(sum, none, red, phase);
     phase ^= 1;
@@ -160,11 +162,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (lane + i * NT) * 8;
+      float q = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         f[i][j] -= mean;
-        if (c + j < cols) ss = fmaf(f[i][j], f[i][j], ss);
+        if (RAGGED && c + j >= cols) f[i][j] = 0.f;
+        q = fmaf(f[i][j], f[i][j], q);
       }
+      ss += c < cols ? q : 0.f;
     }
     block_sum2<NT>(ss, none, red, phase);
     phase ^= 1;
@@ -179,17 +184,17 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
       const Raw8<T> o = narrow<T>(f[i]);
-      if (y) store8(y + row * a.ldy + c, o, cols - c);
+      if (y) store_chunk<RAGGED>(y + row * a.ldy + c, o, cols - c);
       if (a.y_codes) {
         // the form of y as it is stored; columns past the last are 0
         widen(o, f[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c + j >= cols) f[i][j] = 0.f;
+          if (RAGGED ? c + j >= cols : c >= cols) f[i][j] = 0.f;
       }
     }
     if (a.y_codes)
-      pack_row<T, NT, R>(f, lane, pitch, groups, G, a.y_codes + row * pitch,
+      pack_row<T, NT, R>(f, lane, pitch, groups, Glog, a.y_codes + row * pitch,
                          a.y_steps + row * groups, redm);
     row = next;
     if (row >= rows) return;
@@ -244,9 +249,10 @@ struct XChunk;
 template <typename T>
 struct XChunk<T, false> {
   Raw8<T> raw;
+  template <bool RAGGED>
   __device__ __forceinline__ void load(const LayerNormBackArgs& a, int64_t row, int c,
                                        int cols, int, int, int) {
-    raw = load8((const T*)a.x + row * a.ldx + c, cols - c);
+    raw = load_chunk<RAGGED>((const T*)a.x + row * a.ldx + c, cols - c);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const { widen(raw, f); }
 };
@@ -254,6 +260,7 @@ template <typename T>
 struct XChunk<T, true> {
   uint2 w;
   float step;
+  template <bool RAGGED>
   __device__ __forceinline__ void load(const LayerNormBackArgs& a, int64_t row, int c,
                                        int cols, int pitch, int groups, int glog) {
     w = make_uint2(0, 0);
@@ -269,7 +276,7 @@ struct XChunk<T, true> {
 // Streams of NT threads walk the rows; BT / NT streams share a workgroup and
 // add their gradients in LDS, stream by stream.  Partial sums of workgroup b:
 // ws[b][0][cols] (weight), ws[b][1][cols] (bias).  GRAD = false: dx only.
-template <typename T, int NT, int R, int BT, bool FORM, bool GRAD>
+template <typename T, int NT, int R, int BT, bool FORM, bool GRAD, bool RAGGED>
 __global__ __launch_bounds__(BT) void k_layer_norm_backward(
     int64_t rows, int cols, int pitch, int groups, int glog, LayerNormBackArgs a) {
   constexpr int S = BT / NT;
@@ -295,8 +302,8 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
-        rdy[i] = load8((const T*)a.dy + row * a.lddy + c, cols - c);
-        rx[i].load(a, row, c, cols, pitch, groups, glog);
+        rdy[i] = load_chunk<RAGGED>((const T*)a.dy + row * a.lddy + c, cols - c);
+        rx[i].template load<RAGGED>(a, row, c, cols, pitch, groups, glog);
       }
       mean = a.mean[row];
       rstd = a.rstd[row];
@@ -309,17 +316,22 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
     const int64_t row = base + stream;
     const bool live = row < rows;
     float d[R][8], xh[R][8], s1 = 0.f, s2 = 0.f;
-    const float mu = mean, rs = rstd;
+    const float mu = live ? mean : 0.f, rs = live ? rstd : 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (lane + i * NT) * 8;
       widen(rdy[i], d[i]);
       rx[i].get(xh[i]);
+      if (!live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[i][j] = xh[i][j] = 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool in = live && c + j < cols;
-        xh[i][j] = in ? (xh[i][j] - mu) * rs : 0.f;
-        d[i][j] = in ? d[i][j] : 0.f;
+        // past the end dy is 0 and (x - mu) is not: only dy counts there, but
+        // a NaN or an infinity in mu or rs has to stay out
+        xh[i][j] = (xh[i][j] - mu) * rs;
+        if (RAGGED ? c + j >= cols : c >= cols) xh[i][j] = 0.f;
         if constexpr (GRAD) {
           gw[i][j] = fmaf(d[i][j], xh[i][j], gw[i][j]);
           gb[i][j] += d[i][j];
@@ -339,7 +351,7 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
         const int c = (lane + i * NT) * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[i][j] = rs * (d[i][j] - fmaf(xh[i][j], m2, m1));
-        store8((T*)a.dx + row * a.lddx + c, narrow<T>(d[i]), cols - c);
+        store_chunk<RAGGED>((T*)a.dx + row * a.lddx + c, narrow<T>(d[i]), cols - c);
       }
     }
   }
@@ -395,7 +407,7 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
     XChunk<T, FORM> rx;
     for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
       widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
-      rx.load(a, row, c, cols, pitch, groups, glog);
+      rx.template load<true>(a, row, c, cols, pitch, groups, glog);
       rx.get(xh);
       load_vec(a.weight, c, cols, 1.f, w);
 #pragma unroll
@@ -411,7 +423,7 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
     const float m1 = s1 / (float)cols, m2 = s2 / (float)cols;
     for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
       widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
-      rx.load(a, row, c, cols, pitch, groups, glog);
+      rx.template load<true>(a, row, c, cols, pitch, groups, glog);
       rx.get(xh);
       load_vec(a.weight, c, cols, 1.f, w);
 #pragma unroll
@@ -432,7 +444,7 @@ __global__ __launch_bounds__(256) void k_layer_norm_columns(
     const float mu = a.mean[row], rs = a.rstd[row];
     widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
     XChunk<T, FORM> rx;
-    rx.load(a, row, c, cols, pitch, groups, glog);
+    rx.template load<true>(a, row, c, cols, pitch, groups, glog);
     rx.get(xh);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -500,6 +512,13 @@ int back_streams(const ActDims& A, int nt, int bt) {
   return (int)(need < most ? need : most);
 }
 
+int glog_of(const ActDims& A) {
+  int g = 31;
+  if (!A.whole_row)
+    for (g = 0; (1 << g) < A.group;) ++g;
+  return g;
+}
+
 template <typename T>
 struct Forward {
   const ActDims& A;
@@ -509,8 +528,10 @@ struct Forward {
   void operator()() {
     constexpr int BT = NT < 256 ? 256 : NT, PER = BT / NT;
     const int64_t need = (A.rows + PER - 1) / PER, most = (int64_t)kCus * (2048 / BT);
-    k_layer_norm<T, NT, R><<<(unsigned)(need < most ? need : most), BT, 0, st>>>(
-        A.rows, (int)A.cols, (int)A.pitch, A.groups, A.whole_row ? 0 : A.group / 8, a);
+    const unsigned g = (unsigned)(need < most ? need : most);
+    auto* k = A.cols % 8 ? k_layer_norm<T, NT, R, true> : k_layer_norm<T, NT, R, false>;
+    k<<<g, BT, 0, st>>>(A.rows, (int)A.cols, (int)A.pitch, A.groups,
+                        A.whole_row ? -1 : glog_of(A) - 3, a);
   }
 };
 
@@ -525,12 +546,6 @@ int forward_t(const ActDims& A, const LayerNormArgs& a, hipStream_t st) {
   return (int)hipGetLastError();
 }
 
-int glog_of(const ActDims& A) {
-  int g = 31;
-  if (!A.whole_row)
-    for (g = 0; (1 << g) < A.group;) ++g;
-  return g;
-}
 
 template <typename T, bool FORM, bool GRAD>
 struct Backward {
@@ -543,8 +558,10 @@ struct Backward {
     constexpr int BT = kBackThreads<NT>, S = BT / NT;
     *parts = back_streams(A, NT, BT);
     const size_t lds = S > 1 && GRAD ? sizeof(float) * NT * R * 8 : 0;
-    k_layer_norm_backward<T, NT, R, BT, FORM, GRAD><<<(unsigned)*parts, BT, lds, st>>>(
-        A.rows, (int)A.cols, (int)A.pitch, A.groups, glog_of(A), a);
+    auto* k = A.cols % 8 ? k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, true>
+                         : k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, false>;
+    k<<<(unsigned)*parts, BT, lds, st>>>(A.rows, (int)A.cols, (int)A.pitch, A.groups,
+                                         glog_of(A), a);
   }
 };
 
