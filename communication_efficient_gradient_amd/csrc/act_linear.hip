@@ -43,20 +43,6 @@ struct LinearArgs {
   int mtiles, ntiles;
 };
 
-// Tile of a workgroup.  Workgroups go round the eight XCDs in turn; each XCD
-// gets a run of consecutive tiles, taken in columns of up to eight tiles of
-// tokens, so that what its L2 holds is used by many of its workgroups.
-__device__ __forceinline__ void tile_of(int mtiles, int ntiles, int* mt, int* nt) {
-  const int total = mtiles * ntiles, id = (int)blockIdx.x;
-  const int xcd = id % 8, per = total / 8, more = total % 8;
-  const int t = xcd * per + min(xcd, more) + id / 8;
-  const int strip = t / (8 * ntiles), first = strip * 8;
-  const int h = min(8, mtiles - first);
-  const int in = t - first * ntiles;
-  *mt = first + in % h;
-  *nt = in / h;
-}
-
 // A tile of BM tokens by BN outputs per workgroup, WM by WN of it per wave, in
 // k-tiles of BK codes.  An LDS row is BK bytes in CH 16-byte chunks, chunk j of
 // row r at place j ^ (r / (16 / CH) % CH): sixteen lanes that read one chunk of
@@ -71,11 +57,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
-  int mt, nt;
-  tile_of(a.mtiles, a.ntiles, &mt, &nt);
-  const int64_t m0 = (int64_t)mt * BM;
-  const int n0 = nt * BN;
-  const int kt0 = (int)blockIdx.z * a.per;
+  const Tile tile = tile_of(a.mtiles, a.ntiles);
+  const int64_t m0 = (int64_t)tile.i * BM;
+  const int n0 = tile.j * BN;
+  const int kt0 = tile.split * a.per;
   const int nk = min(a.per, div_up(a.pitch, BK) - kt0);
 
   // copies: a wave instruction fills RPI rows.  Rows past the end lie behind
@@ -222,7 +207,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int n = n0 + wn + i * 32 + q * 8 + lane / 32 * 4;
-        int32_t* p = a.ws + ((int64_t)blockIdx.z * a.rows + m) * a.out + n;
+        int32_t* p = a.ws + ((int64_t)tile.split * a.rows + m) * a.out + n;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (n + r < a.out) p[r] = acc[i][j][q * 4 + r];
@@ -339,7 +324,7 @@ int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
   }
   a.mtiles = div_up(A.rows, tile);
   a.ntiles = div_up(a.out, tile);
-  const dim3 g(a.mtiles * a.ntiles, 1, a.splits);
+  const unsigned g = (unsigned)(a.mtiles * a.ntiles * a.splits);
   if (tile == 256) k_act_linear<T, 256, 256, 128, 64, 128><<<g, 512, 0, st>>>(a);
   else k_act_linear<T, 128, 128, 64, 64, 128><<<g, 256, 0, st>>>(a);
   int rc = (int)hipGetLastError();

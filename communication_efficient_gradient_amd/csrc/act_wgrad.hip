@@ -35,10 +35,14 @@ struct WgradArgs {
   const float* steps;
   float beta;
   float *dw, *db;      // results
-  float *ws_w, *ws_b;  // parts: [split][out][cols], [split][ctiles][out]
+  float *ws_w, *ws_b;  // parts: [split][out * cols], [split][turns][out], in quads
   int splits, otiles, ctiles;
+  int turns;           // tiles of a row that share the bias's sums
   int64_t per;         // tokens of a split, a multiple of 64
 };
+
+// Length of a part in the workspace: whole quads of floats.
+__host__ __device__ inline int64_t quads(int64_t n) { return (n + 3) / 4 * 4; }
 
 // Byte offset of 32-byte chunk `ch` (16 columns) of token row t in a tile of W
 // columns.  One transposing read takes two neighbouring chunks of rows 0..3
@@ -66,20 +70,6 @@ __device__ __forceinline__ bf16x8 operand(LdsPtr p) {
       bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Tile of a workgroup: workgroups go round the eight XCDs in turn; each XCD
-// gets a run of consecutive tiles, in columns of up to eight tiles of output
-// features, so that its workgroups share what its L2 holds.
-__device__ __forceinline__ void tile_of(int otiles, int ctiles, int* ot, int* ct) {
-  const int total = otiles * ctiles, id = (int)blockIdx.x;
-  const int xcd = id % 8, per = total / 8, more = total % 8;
-  const int t = xcd * per + min(xcd, more) + id / 8;
-  const int strip = t / (8 * ctiles), first = strip * 8;
-  const int h = min(8, otiles - first);
-  const int in = t - first * ctiles;
-  *ot = first + in % h;
-  *ct = in / h;
-}
-
 // A tile of BO output features by BC columns per workgroup, WO by WC of it per
 // wave, in steps of BK tokens.  While a step's products run, dy of the next
 // step is copied to LDS (COPY: straight from memory, which needs 16-byte
@@ -96,10 +86,10 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wo = wave % (BO / WO) * WO, wc = wave / (BO / WO) * WC;
-  int ot, ct;
-  tile_of(a.otiles, a.ctiles, &ot, &ct);
+  const Tile tile = tile_of(a.otiles, a.ctiles);
+  const int ot = tile.i, ct = tile.j;
   const int o0 = ot * BO, c0 = ct * BC;
-  const int64_t t0 = (int64_t)blockIdx.z * a.per;
+  const int64_t t0 = (int64_t)tile.split * a.per;
   const int64_t t1 = min(t0 + a.per, a.rows);
   const int steps = (int)((t1 - t0 + BK - 1) / BK);
 
@@ -198,9 +188,9 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
         __builtin_bit_cast(u32x4, narrow<__bf16>(f));
   };
 
-  // The bias's sums are shared out over the tiles of a row: tile ct takes the
-  // steps st with st % ctiles == ct.
-  const bool bias = a.db != nullptr;
+  // The bias's sums are shared out over the tiles of a row: tile ct < turns
+  // takes the steps st with st % turns == ct.
+  const bool bias = a.db != nullptr && ct < a.turns;
   auto sum_dy = [&](LdsPtr from) {
     constexpr int N = BK * BO / 8 / TH;
 #pragma unroll
@@ -241,14 +231,14 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
     for (int j = 0; j < CT; ++j) fb[to][j] = operand<BC>(q + pb[j]);
   };
 
-  int turn = 0;  // st % ctiles
+  int turn = 0;  // st % turns
   // Step st from (now_a, now_b), with step st + 1 prepared in (next_a, next_b)
   // and the codes of step st + 2 loaded.  All four are restrict: reads and
   // writes here do not wait for the copies on their way to next_a.  Past the
   // last step zeros are prepared.
   auto step = [&](int st, LdsPtr __restrict__ now_a, LdsPtr __restrict__ now_b,
                   LdsPtr __restrict__ next_a, LdsPtr __restrict__ next_b) {
-    turn = turn + 1 == a.ctiles ? 0 : turn + 1;
+    turn = turn + 1 == a.turns ? 0 : turn + 1;
     const bool sum = bias && turn == ct && st + 1 < steps;
     if constexpr (COPY) copy_dy(next_a);
     next_codes();
@@ -331,7 +321,7 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   // a lane holds one column of sixteen output features per 32 x 32 tile, so a
   // store instruction writes two whole 128-byte lines
   const bool parts = a.splits > 1;
-  float* dw = parts ? a.ws_w + (int64_t)blockIdx.z * a.out * a.cols : a.dw;
+  float* dw = parts ? a.ws_w + tile.split * quads((int64_t)a.out * a.cols) : a.dw;
   const float beta = parts ? 0.f : a.beta;
 #pragma unroll
   for (int j = 0; j < CT; ++j) {
@@ -354,7 +344,7 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
 #pragma unroll
     for (int j = 0; j < 8; ++j) sh[tid / LPR * BO + tid % LPR * 8 + j] = bsum[j];
     __syncthreads();
-    const bool one = a.splits == 1 && a.ctiles == 1;
+    const bool one = a.splits == 1 && a.turns == 1;
     for (int o = tid; o < BO && o0 + o < a.out; o += TH) {
       float s = 0.f;
 #pragma unroll
@@ -363,61 +353,97 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
         float* q = a.db + o0 + o;
         *q = a.beta == 0.f ? s : fmaf(a.beta, *q, s);
       } else {
-        a.ws_b[((int64_t)blockIdx.z * a.ctiles + ct) * a.out + o0 + o] = s;
+        a.ws_b[((int64_t)tile.split * a.turns + ct) * quads(a.out) + o0 + o] = s;
       }
     }
   }
 }
 
-// Adds the parts of dw (splits of them) and db (splits * ctiles), in order.
+// Adds the parts of dw (splits of them) and db (splits * turns), in order:
+// four neighbouring results per thread, the loads of eight parts at a time
+// (whole quads: parts are padded to them and a quad never straddles dw's end).
 __global__ __launch_bounds__(256) void k_act_wgrad_join(WgradArgs a) {
   const int64_t n = a.splits > 1 ? (int64_t)a.out * a.cols : 0;
-  const int64_t total = n + (a.db ? a.out : 0);
+  const int64_t qw = (n + 3) / 4, total = qw + (a.db ? (a.out + 3) / 4 : 0);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
-    const bool w = i < n;
-    const float* q = w ? a.ws_w + i : a.ws_b + (i - n);
-    const int64_t stride = w ? n : a.out;
-    const int parts = w ? a.splits : a.splits * a.ctiles;
-    float s = q[0];
-    for (int k = 1; k < parts; ++k) s += q[k * stride];
-    float* o = w ? a.dw + i : a.db + (i - n);
-    *o = a.beta == 0.f ? s : fmaf(a.beta, *o, s);
+    const bool w = i < qw;
+    const int64_t e = (w ? i : i - qw) * 4, len = w ? n : a.out;
+    const float* q = (w ? a.ws_w : a.ws_b) + e;
+    const int64_t stride = quads(len);
+    const int parts = w ? a.splits : a.splits * a.turns;
+    f32x4 s = *(const f32x4*)q;
+    int k = 1;
+    for (; k + 8 <= parts; k += 8) {
+      f32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = *(const f32x4*)(q + (k + u) * stride);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+    for (; k < parts; ++k) s += *(const f32x4*)(q + k * stride);
+    float* o = (w ? a.dw : a.db) + e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (e + j < len) o[j] = a.beta == 0.f ? s[j] : fmaf(a.beta, o[j], s[j]);
   }
 }
 
 struct Plan {
-  int tile, splits, otiles, ctiles;
+  int tile, splits, otiles, ctiles, turns;
   int64_t per;
 };
 
+// The tile's side and the number of splits by an estimate of the time in
+// microseconds: rounds of workgroups (one 256 x 256 tile or two 128 x 128
+// tiles per CU), a step of 64 tokens each, what a tile costs besides, and the
+// parts' way through memory and back.  Measured (bf16, whole call): 16384 x
+// 2048 x 2048 tokens x out x cols 158 us with 256-tiles and 4 splits, 200 with
+// 128-tiles and 2; 8192 x 1024 x 1024 47 us with 256 and 16, 43.5 with 128 and
+// 8; 512 x 1024 x 4096 28 and 19 us unsplit; 8192 x 256 x 256 28.5 and 18 us
+// with 16 splits.
 Plan plan_wgrad(const ActDims& A, int64_t out) {
-  Plan p;
-  p.tile = ((out + 255) / 256) * ((A.cols + 255) / 256) >= 128 ? 256 : 128;
-  p.otiles = div_up(out, p.tile);
-  p.ctiles = div_up(A.cols, p.tile);
-  const int64_t tiles = (int64_t)p.otiles * p.ctiles, steps = (A.rows + 63) / 64;
-  const int64_t fill = p.tile == 256 ? kCus : 2 * kCus;
-  int64_t splits = tiles >= fill ? 1 : fill / tiles;
-  if (splits > steps / 4) splits = steps / 4 > 0 ? steps / 4 : 1;
-  p.per = steps == 0 ? 64 : (steps + splits - 1) / splits * 64;
-  p.splits = steps == 0 ? 1 : div_up(steps * 64, p.per);
-  return p;
+  const int64_t steps = (A.rows + 63) / 64;
+  const double big_step = A.dtype == GQ_BF16 ? 1.9 : A.dtype == GQ_F16 ? 4.4 : 5.0;
+  const double small_step = A.dtype == GQ_BF16 ? 1.45 : A.dtype == GQ_F16 ? 3.0 : 3.4;
+  Plan best = {};
+  double least = 1e30;
+  for (int tile = 128; tile <= 256; tile *= 2) {
+    const int64_t ot = (out + tile - 1) / tile, ct = (A.cols + tile - 1) / tile;
+    for (int64_t s = 1; s <= 32 && (s == 1 || s * 2 <= steps); ++s) {
+      const int64_t per = s == 1 ? (steps > 0 ? steps : 1) : (steps + s - 1) / s;
+      const int64_t groups = ot * ct * s, slots = tile == 256 ? kCus : 2 * kCus;
+      double step = tile == 256 ? big_step : small_step;
+      if (tile == 128 && groups <= kCus) step *= 0.7;  // alone on its CU
+      double t = (double)((groups + slots - 1) / slots) *
+                 ((double)per * step + (tile == 256 ? 8.0 : 5.0));
+      if (s > 1) t += 4.0 + 8.0 * (double)(s * out) * (double)A.cols / 6.5e6;
+      if (t < least) {
+        least = t;
+        best = {tile, (int)(((steps > 0 ? steps : 1) + per - 1) / per), (int)ot, (int)ct,
+                (int)ct, per * 64};
+      }
+    }
+  }
+  // Shared out, the bias's sums need a second launch to join them (5 us); of
+  // up to 32 steps one tile takes all (0.15 us each).
+  if (best.splits == 1 && steps <= 32) best.turns = 1;
+  return best;
 }
 
 template <typename T, bool COPY, int BK>
 void wgrad_t(const WgradArgs& a, int tile, hipStream_t st) {
-  const dim3 g(a.otiles * a.ctiles, 1, a.splits);
+  const unsigned g = (unsigned)(a.otiles * a.ctiles * a.splits);
   if (tile == 256) k_act_wgrad<T, COPY, 256, 256, 128, 64, BK><<<g, 512, 0, st>>>(a);
-  else k_act_wgrad<T, COPY, 128, 128, 64, 64, BK><<<g, 256, 0, st>>>(a);
+  else k_act_wgrad<T, COPY, 128, 128, 64, 32, BK><<<g, 512, 0, st>>>(a);
 }
 
 }  // namespace
 
 int64_t act_wgrad_workspace(const ActDims& A, int64_t out) {
   const Plan p = plan_wgrad(A, out);
-  const int64_t w = p.splits > 1 ? (int64_t)p.splits * out * A.cols : 0;
-  const int64_t b = p.splits * p.ctiles > 1 ? (int64_t)p.splits * p.ctiles * out : 0;
+  const int64_t w = p.splits > 1 ? p.splits * quads(out * A.cols) : 0;
+  const int64_t b = p.splits * p.turns > 1 ? (int64_t)p.splits * p.turns * quads(out) : 0;
   return 4 * (w + b);
 }
 
@@ -429,11 +455,11 @@ int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy
   if (!A.whole_row)
     for (glog = 0; (1 << glog) < A.group;) ++glog;
   float* w = (float*)ws;
-  const int64_t wn = p.splits > 1 ? (int64_t)p.splits * out * A.cols : 0;
+  const int64_t wn = p.splits > 1 ? p.splits * quads(out * A.cols) : 0;
   const WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, glog,
                        dy,     lddy,     codes,       steps,        beta,     dw,
                        db,     w,        w + wn,      p.splits,     p.otiles, p.ctiles,
-                       p.per};
+                       p.turns, p.per};
   // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
   const bool copy = A.dtype == GQ_BF16 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
                     lddy < (1 << 23) &&
@@ -443,8 +469,9 @@ int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy
   else if (copy) wgrad_t<__bf16, true, 64>(a, p.tile, st);
   else wgrad_t<__bf16, false, 64>(a, p.tile, st);
   int rc = (int)hipGetLastError();
-  if (rc == 0 && (p.splits > 1 || (db && p.splits * p.ctiles > 1))) {
-    const int64_t n = (p.splits > 1 ? out * A.cols : 0) + out, b = (n + 255) / 256;
+  if (rc == 0 && (p.splits > 1 || (db && p.splits * p.turns > 1))) {
+    const int64_t n = (p.splits > 1 ? quads(out * A.cols) : 0) + quads(out);
+    const int64_t b = (n / 4 + 255) / 256;
     k_act_wgrad_join<<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(a);
     rc = (int)hipGetLastError();
   }
