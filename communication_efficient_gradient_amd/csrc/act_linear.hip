@@ -230,70 +230,118 @@ __global__ __launch_bounds__(256) void k_act_linear_join(LinearArgs a) {
   }
 }
 
-// Few tokens (up to 16 * MT): the weight is read once, straight into the
-// products' operand layout (16 codes of one output per lane, 16 outputs by 64
-// codes per instruction), and the tokens' codes come from L2.  A workgroup
-// takes 16 outputs; its eight waves take turns of U * 64 codes along the sum
-// and add up in LDS.  One pass over the weight is all there is to wait for:
-// U loads per wave are in flight at once.
+// Few tokens.  A workgroup takes 16 * MT tokens by 16 * NT outputs; its eight
+// waves take turns of U * 64 codes along the sum and add up in LDS.  Operands
+// come straight from memory (the weight, once where MT covers the tokens) and
+// L2 in the products' layout, 16 codes of one row per lane, 16 rows by 64 codes
+// per instruction: nothing waits for a barrier until the sums are joined, and
+// U steps of loads per wave are in flight at once.
 constexpr int kFewWaves = 8;
 
-template <typename T, int MT, int U>
+template <typename T, int MT, int NT, int U>
 __global__ __launch_bounds__(kFewWaves * 64) void k_act_linear_few(LinearArgs a) {
-  __shared__ __attribute__((aligned(16))) int32_t sums[kFewWaves][MT][256];
+  constexpr int HALF = kFewWaves / 2, E = MT * NT * 256;
+  __shared__ __attribute__((aligned(16))) int32_t sums[HALF][E];
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int n0 = (int)blockIdx.x * 16;
+  const int n0 = (int)blockIdx.x * (16 * NT);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
   const BufferRange w = range_of(a.w_codes + (int64_t)n0 * a.pitch,
                                  (int64_t)(a.out - n0) * a.pitch);
-  const BufferRange x = range_of(a.codes, a.rows * a.pitch);
+  const BufferRange x = range_of(a.codes + m0 * a.pitch, (a.rows - m0) * a.pitch);
   const int row = lane % 16 * a.pitch, col = lane / 16 * 16;
-  i32x4 acc[MT];
+  i32x4 acc[NT][MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = i32x4{0, 0, 0, 0};
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
   for (int k = wave * (U * 64); k < a.pitch; k += kFewWaves * U * 64) {
-    i32x4 fw[U], fx[U][MT];
+    i32x4 fw[U][NT], fx[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // past the pitch lies the next row: those chunks are zeros
-      const int c = k + u * 64 + col;
-      fw[u] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                            w, c < a.pitch ? row + c : kPastEnd, 0, 0));
-    }
+      const int c = k + u * 64 + col, at = c < a.pitch ? row + c : kPastEnd;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = k + u * 64 + col;
+      for (int j = 0; j < NT; ++j)
+        fw[u][j] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(w, at, j * 16 * a.pitch, 0));
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         fx[u][i] = __builtin_bit_cast(
-            i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       x, c < a.pitch ? row + i * 16 * a.pitch + c : kPastEnd, 0, 0));
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(x, at + i * 16 * a.pitch, 0, 0));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u], fx[u][i], acc[i], 0, 0, 0);
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          acc[j][i] =
+              __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][j], fx[u][i], acc[j][i], 0, 0, 0);
   }
-  // a lane holds four consecutive outputs of token lane % 16
+  // a lane holds four consecutive outputs of token lane % 16; kept as
+  // [token][output], 16 * NT outputs to a token
+  auto at = [&](int j, int i) {
+    return (i * 16 + lane % 16) * (16 * NT) + j * 16 + lane / 16 * 4;
+  };
+  if (wave >= HALF) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    *reinterpret_cast<i32x4*>(&sums[wave][i][lane % 16 * 16 + lane / 16 * 4]) = acc[i];
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        *reinterpret_cast<i32x4*>(&sums[wave - HALF][at(j, i)]) = acc[j][i];
+  }
   __syncthreads();
+  if (wave < HALF) {
 #pragma unroll
-  for (int e = (int)threadIdx.x; e < MT * 256; e += kFewWaves * 64) {
-    const int64_t m = e / 16;
-    const int n = n0 + e % 16;
-    int32_t s = 0;
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int v = 0; v < kFewWaves; ++v) s += sums[v][e / 256][e % 256];
-    if (m < a.rows && n < a.out)
-      ((T*)a.y)[m * a.ldy + n] =
-          (T)((float)s * a.steps[m] * a.w_steps[n] + (a.bias ? a.bias[n] : 0.f));
+      for (int i = 0; i < MT; ++i) {
+        i32x4* p = reinterpret_cast<i32x4*>(&sums[wave][at(j, i)]);
+        *p += acc[j][i];
+      }
+  }
+  __syncthreads();
+  for (int e = (int)threadIdx.x * 4; e < E; e += kFewWaves * 64 * 4) {
+    const int64_t m = m0 + e / (16 * NT);
+    const int n = n0 + e % (16 * NT);
+    if (m >= a.rows || n >= a.out) continue;
+    i32x4 s = *reinterpret_cast<const i32x4*>(&sums[0][e]);
+#pragma unroll
+    for (int v = 1; v < HALF; ++v) s += *reinterpret_cast<const i32x4*>(&sums[v][e]);
+    const float step = a.steps[m];
+    T o[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int c = min(n + r, a.out - 1);
+      o[r] = (T)((float)s[r] * step * a.w_steps[c] + (a.bias ? a.bias[c] : 0.f));
+    }
+    T* y = (T*)a.y + m * a.ldy + n;
+    if (n + 4 <= a.out) {
+      __builtin_memcpy(y, o, sizeof(o));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < a.out) y[r] = o[r];
+    }
   }
 }
 
-constexpr int kFewRows = 64;
+// Up to 512 of the small tiles (64 tokens by 32 outputs: two a CU) the tiled
+// kernel's barriers and the join of its splits cost more than operands read
+// oftener.  Measured, small against tiled: 128 x 4096 x 4096 (tokens x out x
+// cols) 17 and 27 us, 203 x 2050 x 4100 20 and 25, 300 x 1024 x 1024 8.5 and
+// 16, 256 x 4096 x 4096 27 and 29.5; with 1024 tiles, 512 x 4096 x 4096, 49
+// and 34 us.
+bool few_tokens(const ActDims& A, int64_t out) {
+  return A.rows <= 64 || ((A.rows + 63) / 64) * ((out + 31) / 32) <= 512;
+}
+
+template <typename T, int MT, int NT, int U>
+void few(const LinearArgs& a, hipStream_t st) {
+  const dim3 g(div_up(a.out, 16 * NT), div_up(a.rows, 16 * MT));
+  k_act_linear_few<T, MT, NT, U><<<g, kFewWaves * 64, 0, st>>>(a);
+}
 
 struct Plan {
   int splits, per;
@@ -303,7 +351,7 @@ struct Plan {
 Plan plan_linear(const ActDims& A, int64_t out) {
   const int kt = div_up(A.pitch, 128);
   Plan p = {1, kt, 0};
-  if (A.rows <= kFewRows) return p;
+  if (few_tokens(A, out)) return p;
   p.tile = ((A.rows + 255) / 256) * ((out + 255) / 256) >= 128 ? 256 : 128;
   const int64_t tiles = ((A.rows + p.tile - 1) / p.tile) * ((out + p.tile - 1) / p.tile);
   int splits = tiles >= kCus ? 1 : (int)(kCus / tiles);
@@ -315,11 +363,11 @@ Plan plan_linear(const ActDims& A, int64_t out) {
 
 template <typename T>
 int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
-  if (A.rows <= kFewRows) {
-    const int g = div_up(a.out, 16), t = kFewWaves * 64;
-    if (A.rows <= 16) k_act_linear_few<T, 1, 8><<<g, t, 0, st>>>(a);
-    else if (A.rows <= 32) k_act_linear_few<T, 2, 4><<<g, t, 0, st>>>(a);
-    else k_act_linear_few<T, 4, 4><<<g, t, 0, st>>>(a);
+  if (few_tokens(A, a.out)) {
+    if (A.rows <= 16) few<T, 1, 1, 8>(a, st);
+    else if (A.rows <= 32) few<T, 2, 1, 4>(a, st);
+    else if (A.rows <= 64) few<T, 2, 2, 4>(a, st);
+    else few<T, 4, 2, 2>(a, st);
     return (int)hipGetLastError();
   }
   a.mtiles = div_up(A.rows, tile);

@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kBlock) void k_act_pack_lanes(
   for (int i = 0; i < UNITS; ++i, next_unit(&u, turns)) {
     const int64_t row = u.rows0 * per + in;
     const int c = (u.turn * tpr + lane) * 8;
-    raw[i] = load_chunk<RAGGED>(x + row * ldx + c, row < rows ? cols - c : 0);
+    raw[i] = load_chunk<RAGGED>(x + row * ldx, c, row < rows ? cols : 0);
   }
 #pragma unroll
   for (int i = 0; i < UNITS; ++i, next_unit(&v, turns)) {
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (lane + i * NT) * 8;
-      raw[i] = load_chunk<RAGGED>(x + row * ldx + lo + c, s < total ? n - c : 0);
+      raw[i] = load_chunk<RAGGED>(x + row * ldx, lo + c, s < total ? lo + n : 0);
     }
   };
   if constexpr (R > 0) fetch(at);

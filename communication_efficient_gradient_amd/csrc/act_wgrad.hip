@@ -124,8 +124,8 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   auto load_dy = [&](int st, int i) {
     const int q = i * TH + tid, t = q / LPR, p = q % LPR;
     const int64_t row = t0 + (int64_t)st * BK + t;
-    const int valid = row < t1 ? a.out - o0 - p * 8 : 0;
-    ra[i] = load8((const T*)dy + (row < t1 ? row : 0) * a.lddy + p * 8, valid);
+    const T* r = (const T*)a.dy + (row < t1 ? row : 0) * a.lddy;
+    ra[i] = load_chunk<true>(r, o0 + p * 8, row < t1 ? a.out : 0);
   };
   float bsum[8] = {};
   auto write_dy = [&](LdsPtr to, bool sum, int i) {

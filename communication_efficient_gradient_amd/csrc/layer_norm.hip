@@ -60,13 +60,14 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
   return m;
 }
 
+template <bool RAGGED>
 __device__ __forceinline__ void load_vec(const float* __restrict__ p, int c, int cols,
                                          float none, float (&f)[8]) {
   if (p == nullptr) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = none;
   } else {
-    widen(load8(p + c, cols - c), f);
+    widen(load_chunk<RAGGED>(p, c, cols), f);
   }
 }
 
@@ -125,14 +126,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int c = (lane + i * NT) * 8;
-    load_vec(a.weight, c, cols, 1.f, w[i]);
-    load_vec(a.bias, c, cols, 0.f, b[i]);
+    load_vec<RAGGED>(a.weight, c, cols, 1.f, w[i]);
+    load_vec<RAGGED>(a.bias, c, cols, 0.f, b[i]);
   }
   Raw8<T> raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int c = (lane + i * NT) * 8;
-    raw[i] = load_chunk<RAGGED>(x + row * a.ldx + c, cols - c);
+    raw[i] = load_chunk<RAGGED>(x + row * a.ldx, c, cols);
   }
   const float n = (float)cols;
   int phase = 0;
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
-        raw[i] = load_chunk<RAGGED>(x + next * a.ldx + c, cols - c);
+        raw[i] = load_chunk<RAGGED>(x + next * a.ldx, c, cols);
       }
     }
     if (a.x_codes)
@@ -232,8 +233,8 @@ __global__ __launch_bounds__(1024) void k_layer_norm_long(int64_t rows, int cols
     for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
       float w[8], b[8];
       widen(load8(x + c, cols - c), f);
-      load_vec(a.weight, c, cols, 1.f, w);
-      load_vec(a.bias, c, cols, 0.f, b);
+      load_vec<true>(a.weight, c, cols, 1.f, w);
+      load_vec<true>(a.bias, c, cols, 0.f, b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean) * rstd, w[j], b[j]);
       store8((T*)a.y + row * a.ldy + c, narrow<T>(f), cols - c);
@@ -252,7 +253,7 @@ struct XChunk<T, false> {
   template <bool RAGGED>
   __device__ __forceinline__ void load(const LayerNormBackArgs& a, int64_t row, int c,
                                        int cols, int, int, int) {
-    raw = load_chunk<RAGGED>((const T*)a.x + row * a.ldx + c, cols - c);
+    raw = load_chunk<RAGGED>((const T*)a.x + row * a.ldx, c, cols);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const { widen(raw, f); }
 };
@@ -274,14 +275,14 @@ struct XChunk<T, true> {
 };
 
 // Streams of NT threads walk the rows; BT / NT streams share a workgroup and
-// add their gradients in LDS, stream by stream.  Partial sums of workgroup b:
+// add their gradients in LDS.  Partial sums of workgroup b:
 // ws[b][0][cols] (weight), ws[b][1][cols] (bias).  GRAD = false: dx only.
 template <typename T, int NT, int R, int BT, bool FORM, bool GRAD, bool RAGGED>
 __global__ __launch_bounds__(BT) void k_layer_norm_backward(
     int64_t rows, int cols, int pitch, int groups, int glog, LayerNormBackArgs a) {
   constexpr int S = BT / NT;
   __shared__ float red_all[S][2][2][16];
-  extern __shared__ float part[];  // S > 1: [NT * R * 8]
+  extern __shared__ float part[];  // S > 1: [S][NT * R * 8]
   const int stream = (int)threadIdx.x / NT, lane = (int)threadIdx.x % NT;
   float(*red)[2][16] = red_all[stream];
   // every stream of a workgroup takes the same number of turns (barriers)
@@ -290,7 +291,7 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
   float w[R][8], gw[R][8], gb[R][8];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    load_vec(a.weight, (lane + i * NT) * 8, cols, 1.f, w[i]);
+    load_vec<RAGGED>(a.weight, (lane + i * NT) * 8, cols, 1.f, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) gw[i][j] = gb[i][j] = 0.f;
   }
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
-        rdy[i] = load_chunk<RAGGED>((const T*)a.dy + row * a.lddy + c, cols - c);
+        rdy[i] = load_chunk<RAGGED>((const T*)a.dy + row * a.lddy, c, cols);
         rx[i].template load<RAGGED>(a, row, c, cols, pitch, groups, glog);
       }
       mean = a.mean[row];
@@ -356,39 +357,34 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
     }
   }
   if constexpr (GRAD) {
+    float* o = a.ws + (int64_t)blockIdx.x * 2 * cols;
     if constexpr (S > 1) {
-      // stream by stream, the weight's sums and then the bias's
+      // the streams' sums side by side in LDS, then added in order
+      constexpr int W = NT * R * 8;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        auto& g = k == 0 ? gw : gb;
-        for (int s = 0; s < S; ++s) {
-          if (stream == s) {
+        const auto& g = k == 0 ? gw : gb;
+        if (k > 0) __syncthreads();
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const int c = (lane + i * NT) * 8;
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if (s > 0) g[i][j] += part[c + j];
-                if (s < S - 1) part[c + j] = g[i][j];
-              }
-            }
-          }
-          __syncthreads();
+          for (int j = 0; j < 8; j += 4)
+            *reinterpret_cast<f32x4*>(&part[stream * W + (lane + i * NT) * 8 + j]) =
+                f32x4{g[i][j], g[i][j + 1], g[i][j + 2], g[i][j + 3]};
+        __syncthreads();
+        for (int c = (int)threadIdx.x; c < cols; c += BT) {
+          float t = part[c];
+#pragma unroll
+          for (int s = 1; s < S; ++s) t += part[s * W + c];
+          o[k * cols + c] = t;
         }
       }
-    }
-    if (stream == S - 1) {
-      float* o = a.ws + (int64_t)blockIdx.x * 2 * cols;
+    } else {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
-        Raw8<float> q;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q.v[j] = gw[i][j];
-        store8(o + c, q, cols - c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q.v[j] = gb[i][j];
-        store8(o + cols + c, q, cols - c);
+        store8(o + c, narrow<float>(gw[i]), cols - c);
+        store8(o + cols + c, narrow<float>(gb[i]), cols - c);
       }
     }
   }
@@ -409,7 +405,7 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
       widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
       rx.template load<true>(a, row, c, cols, pitch, groups, glog);
       rx.get(xh);
-      load_vec(a.weight, c, cols, 1.f, w);
+      load_vec<true>(a.weight, c, cols, 1.f, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float v = c + j < cols ? d[j] * w[j] : 0.f;
@@ -425,7 +421,7 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
       widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
       rx.template load<true>(a, row, c, cols, pitch, groups, glog);
       rx.get(xh);
-      load_vec(a.weight, c, cols, 1.f, w);
+      load_vec<true>(a.weight, c, cols, 1.f, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         d[j] = rs * (d[j] * w[j] - fmaf((xh[j] - mu) * rs, m2, m1));
@@ -557,7 +553,7 @@ struct Backward {
   void operator()() {
     constexpr int BT = kBackThreads<NT>, S = BT / NT;
     *parts = back_streams(A, NT, BT);
-    const size_t lds = S > 1 && GRAD ? sizeof(float) * NT * R * 8 : 0;
+    const size_t lds = S > 1 && GRAD ? sizeof(float) * S * NT * R * 8 : 0;
     auto* k = A.cols % 8 ? k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, true>
                          : k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, false>;
     k<<<(unsigned)*parts, BT, lds, st>>>(A.rows, (int)A.cols, (int)A.pitch, A.groups,
