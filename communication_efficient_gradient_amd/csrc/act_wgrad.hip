@@ -6,11 +6,15 @@
 // The sum runs over tokens, the slow axis of both operands, so tiles [t][col]
 // go to LDS as they lie in memory and come out through the transposing LDS
 // read (each lane gets consecutive tokens of one column, the operand layout
-// of the matrix instructions).  x^ = code * step is exact in bf16.  dy in
-// bf16 is used as it is; fp16 is split into two and fp32 into three bf16
-// terms whose sum is the value itself (11 and 24 significant bits), one
-// matrix product each: every product is exact and only the fp32 accumulation
-// rounds.
+// of the matrix instructions).  Every product is exact, only the fp32
+// accumulation rounds:
+//   bf16  x^ = code * step is exact in bf16, dy is used as it is
+//   fp16  x^ is exact in fp16: steps are at most 2^9, and one below 2^-24 comes
+//         with values that are multiples of 2^-24 and kept as they are
+//   fp32  dy is split into three bf16 terms (24 significant bits) whose sum is
+//         the value itself, one matrix product each with x^ in bf16
+#include <type_traits>
+
 #include "act.hpp"
 
 namespace gq {
@@ -21,8 +25,6 @@ typedef GQ_LDS char* LdsPtr;
 
 template <typename T>
 constexpr int kPlanes = 1;
-template <>
-inline constexpr int kPlanes<_Float16> = 2;
 template <>
 inline constexpr int kPlanes<float> = 3;
 
@@ -63,11 +65,36 @@ __device__ __forceinline__ int operand_place(int ch, int lane) {
 }
 
 template <int W>
-__device__ __forceinline__ bf16x8 operand(LdsPtr p) {
+__device__ __forceinline__ s16x8 operand(LdsPtr p) {
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((GQ_LDS s16x4*)p);
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((GQ_LDS s16x4*)(p + 4 * W * 2));
-  return __builtin_bit_cast(
-      bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <typename T>
+__device__ __forceinline__ f32x16 product(s16x8 a, s16x8 b, f32x16 c) {
+  if constexpr (std::is_same_v<T, _Float16>) {
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+}
+
+// Eight values x^ in the products' type (exact in it, see above).
+template <typename T>
+__device__ __forceinline__ u32x4 packed(const float (&f)[8]) {
+  if constexpr (std::is_same_v<T, _Float16>) {
+    u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      r[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(f[2 * j], f[2 * j + 1]));
+    return r;
+  } else {
+    return __builtin_bit_cast(u32x4, narrow<__bf16>(f));
+  }
 }
 
 // A tile of BO output features by BC columns per workgroup, WO by WC of it per
@@ -121,23 +148,40 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   // through registers: pieces of eight columns, BO / 8 per row
   constexpr int AP = COPY ? 1 : BK * BO / 8 / TH;
   Raw8<T> ra[AP];
-  auto load_dy = [&](int st, int i) {
-    const int q = i * TH + tid, t = q / LPR, p = q % LPR;
-    const int64_t row = t0 + (int64_t)st * BK + t;
-    const T* r = (const T*)a.dy + (row < t1 ? row : 0) * a.lddy;
-    ra[i] = load_chunk<true>(r, o0 + p * 8, row < t1 ? a.out : 0);
+  // A short last chunk may run on into the next row, and columns past the
+  // last hold anything; only the steps that reach the last row take care to
+  // stay inside it.
+  const int odd = min(tid % LPR * 8, a.out - 1 - o0);
+  auto load_dy = [&](int st) {
+    const int64_t first = t0 + (int64_t)st * BK + tid / LPR;
+    const T* r = (const T*)dy + first * a.lddy;
+    if (t0 + (int64_t)(st + 1) * BK < a.rows) {
+#pragma unroll
+      for (int i = 0; i < AP; ++i)
+        __builtin_memcpy(&ra[i], r + i * (TH / LPR) * a.lddy + odd, sizeof(ra[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < AP; ++i) {
+        const bool live = first + i * (TH / LPR) < t1;
+        ra[i] = load8(r + i * (TH / LPR) * a.lddy + tid % LPR * 8,
+                      live ? a.out - o0 - tid % LPR * 8 : 0);
+      }
+    }
   };
   float bsum[8] = {};
   auto write_dy = [&](LdsPtr to, bool sum, int i) {
     const int q = i * TH + tid, t = q / LPR, p = q % LPR;
     float v[8];
-    widen(ra[i], v);
+    if (P > 1 || sum) widen(ra[i], v);
     if (sum) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) bsum[j] += v[j];
     }
+    if constexpr (P == 1)
+      *(GQ_LDS u32x4*)(to + place<BO>(t, p / 2) + p % 2 * 16) =
+          __builtin_bit_cast(u32x4, ra[i]);
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
+    for (int k = 0; k < (P > 1 ? P : 0); ++k) {
       u32x4 h;
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
@@ -185,7 +229,7 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
     float f[8];
     decode8(rc[i], rs[i], f);
     *(GQ_LDS u32x4*)(to + place<BC>(t, p / 2) + p % 2 * 16) =
-        __builtin_bit_cast(u32x4, narrow<__bf16>(f));
+        packed<T>(f);
   };
 
   // The bias's sums are shared out over the tiles of a row: tile ct < turns
@@ -197,11 +241,10 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
     for (int i = 0; i < N; ++i) {
       const int q = i * TH + tid, t = q / LPR, p = q % LPR;
       const u32x4 u = *(GQ_LDS u32x4*)(from + place<BO>(t, p / 2) + p % 2 * 16);
+      float v[8];
+      widen(__builtin_bit_cast(Raw8<std::conditional_t<sizeof(T) == 2, T, __bf16>>, u), v);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bsum[2 * j] += __uint_as_float(u[j] << 16);
-        bsum[2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
-      }
+      for (int j = 0; j < 8; ++j) bsum[j] += v[j];
     }
   };
 
@@ -218,7 +261,7 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   for (int i = 0; i < OT; ++i) pa[i] = operand_place<BO>((wo + i * 32) / 16, lane);
 #pragma unroll
   for (int j = 0; j < CT; ++j) pb[j] = operand_place<BC>((wc + j * 32) / 16, lane);
-  bf16x8 fa[2][OT], fb[2][CT];
+  s16x8 fa[2][OT], fb[2][CT];
   // operands of sub-step k (a 16-token block and a plane of dy)
   auto read_a = [&](int to, LdsPtr from, int k) {
     const LdsPtr q = from + k % P * (BK * BO * 2) + k / P * (16 * BO * 2);
@@ -261,7 +304,6 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
 #pragma unroll
           for (int i = k * AP / 2; i < (k + 1) * AP / 2; ++i) {
             write_dy(next_a, sum, i);
-            load_dy(st + 2, i);
           }
         }
 #pragma unroll
@@ -270,12 +312,12 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
           load_codes(i);
         }
       }
+      if (!COPY && k == (KK * P > 2 ? 2 : 1)) load_dy(st + 2);
 #pragma unroll
       for (int i = 0; i < OT; ++i)
 #pragma unroll
         for (int j = 0; j < CT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[k & 1][i], fb[kk & 1][j],
-                                                             acc[i][j], 0, 0, 0);
+          acc[i][j] = product<T>(fa[k & 1][i], fb[kk & 1][j], acc[i][j]);
       // reads and decoding between products
 #pragma unroll
       for (int g = 0; g < OT * CT; ++g) {
@@ -294,13 +336,10 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
     for (int i = 0; i < BP; ++i) load_codes(i);
     next_codes();
     if constexpr (!COPY) {
+      load_dy(0);
 #pragma unroll
-      for (int i = 0; i < AP; ++i) load_dy(0, i);
-#pragma unroll
-      for (int i = 0; i < AP; ++i) {
-        write_dy(a0, bias && ct == 0, i);
-        load_dy(1, i);
-      }
+      for (int i = 0; i < AP; ++i) write_dy(a0, bias && ct == 0, i);
+      load_dy(1);
     }
 #pragma unroll
     for (int i = 0; i < BP; ++i) {
@@ -404,8 +443,8 @@ struct Plan {
 // with 16 splits.
 Plan plan_wgrad(const ActDims& A, int64_t out) {
   const int64_t steps = (A.rows + 63) / 64;
-  const double big_step = A.dtype == GQ_BF16 ? 1.9 : A.dtype == GQ_F16 ? 4.4 : 5.0;
-  const double small_step = A.dtype == GQ_BF16 ? 1.45 : A.dtype == GQ_F16 ? 3.0 : 3.4;
+  const double big_step = A.dtype == GQ_F32 ? 5.0 : 1.9;
+  const double small_step = A.dtype == GQ_F32 ? 3.4 : 1.45;
   Plan best = {};
   double least = 1e30;
   for (int tile = 128; tile <= 256; tile *= 2) {
@@ -431,11 +470,12 @@ Plan plan_wgrad(const ActDims& A, int64_t out) {
   return best;
 }
 
-template <typename T, bool COPY, int BK>
+// BIG, SMALL: tokens of a step for 256- and 128-tiles.
+template <typename T, bool COPY, int BIG, int SMALL>
 void wgrad_t(const WgradArgs& a, int tile, hipStream_t st) {
   const unsigned g = (unsigned)(a.otiles * a.ctiles * a.splits);
-  if (tile == 256) k_act_wgrad<T, COPY, 256, 256, 128, 64, BK><<<g, 512, 0, st>>>(a);
-  else k_act_wgrad<T, COPY, 128, 128, 64, 32, BK><<<g, 512, 0, st>>>(a);
+  if (tile == 256) k_act_wgrad<T, COPY, 256, 256, 128, 64, BIG><<<g, 512, 0, st>>>(a);
+  else k_act_wgrad<T, COPY, 128, 128, 64, 32, SMALL><<<g, 512, 0, st>>>(a);
 }
 
 }  // namespace
@@ -461,13 +501,16 @@ int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy
                        db,     w,        w + wn,      p.splits,     p.otiles, p.ctiles,
                        p.turns, p.per};
   // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
-  const bool copy = A.dtype == GQ_BF16 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
+  const bool copy = A.dtype != GQ_F32 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
                     lddy < (1 << 23) &&
                     out % 8 == 0;
-  if (A.dtype == GQ_F32) wgrad_t<float, false, 32>(a, p.tile, st);
-  else if (A.dtype == GQ_F16) wgrad_t<_Float16, false, 32>(a, p.tile, st);
-  else if (copy) wgrad_t<__bf16, true, 64>(a, p.tile, st);
-  else wgrad_t<__bf16, false, 64>(a, p.tile, st);
+  // Through registers 64-token steps of 256-tiles spill (16384 x 4095 x 4096
+  // bf16: 938 us, 693 with 32); fp32's three terms fill LDS with 32.
+  if (A.dtype == GQ_F32) wgrad_t<float, false, 32, 32>(a, p.tile, st);
+  else if (A.dtype == GQ_F16 && copy) wgrad_t<_Float16, true, 64, 64>(a, p.tile, st);
+  else if (A.dtype == GQ_F16) wgrad_t<_Float16, false, 32, 64>(a, p.tile, st);
+  else if (copy) wgrad_t<__bf16, true, 64, 64>(a, p.tile, st);
+  else wgrad_t<__bf16, false, 32, 64>(a, p.tile, st);
   int rc = (int)hipGetLastError();
   if (rc == 0 && (p.splits > 1 || (db && p.splits * p.turns > 1))) {
     const int64_t n = (p.splits > 1 ? quads(out * A.cols) : 0) + quads(out);

@@ -3,8 +3,8 @@
 Products are exact, so with small whole numbers the sums are exact too and
 have to be equal; otherwise a sum of n products is off by at most 2 n 2^-24
 times the sum of their magnitudes (n counts each term that a value is split
-into: one for bf16, two for fp16, three for fp32; an accumulation may round
-towards zero, hence the 2)."""
+into, three for fp32 and up to two for fp16; an accumulation may round towards
+zero, hence the 2)."""
 import numpy as np
 import pytest
 import torch
@@ -118,6 +118,28 @@ def test_full_range_of_fp32_gradients(gq):
     assert np.array_equal(db.cpu().numpy(), dy[0])
     within(dw, want, 3 * U32 * np.abs(want))
     assert np.array_equal(dw.cpu().numpy()[:, :2], want[:, :2].astype(np.float32))
+
+
+def test_the_ends_of_fp16(gq):
+    """Subnormal and largest values of both operands: one product per sum, so
+    each is off by the accumulation's one rounding at most."""
+    tiny = 2.0 ** -24
+    x = np.zeros((5, 40))
+    x[0, :8] = np.arange(8) * tiny                 # steps below 2^-24
+    x[1, :8] = 65504.0, -65504.0, 40000.0, 1.0, 0.0, 512.0, 60000.0, -33000.0
+    x[2, :8] = 2.0 ** -14 * (1 + np.arange(8) / 8)
+    x[3, 0] = tiny
+    x[4, :8] = 127 * tiny, 128 * tiny, tiny, 0, 3 * tiny, 64 * tiny, 100 * tiny, -tiny
+    codes, steps = A.pack(x, 32, "f16")
+    xr = A.unpack(codes, steps, 40, 32)
+    dy = np.zeros((5, 5))
+    for t, v in enumerate((1.0, 0.5, 3 * tiny, -1023 * tiny, 65504.0)):
+        dy[t, t] = v
+    dw, db, _, _ = run(gq, dy, codes, steps, 40, "f16", 32)
+    want = dy.T @ xr
+    within(dw, want, 2 * U32 * np.abs(want))
+    assert np.count_nonzero(dw.cpu().numpy()) == np.count_nonzero(want)
+    within(db, dy.sum(axis=0), np.zeros(5))
 
 
 def test_values_that_are_not_finite_stay_in_their_sums(gq):
