@@ -248,28 +248,42 @@ __device__ __forceinline__ void copy16_to_lds(
   __builtin_amdgcn_raw_ptr_buffer_load_lds(from, to, 16, each, all, 0, 0);
 }
 
-// Tile (i, j) of i_tiles x j_tiles and split of the sum that a workgroup of a
-// one-dimensional grid takes.  Workgroups go round the eight XCDs in turn, so
-// each XCD gets a run of the splits' tiles one after the other, and within a
+// Tiles (i, j) of i_tiles x j_tiles, for each split of the sum, as a
+// one-dimensional grid takes them.  Workgroups go round the eight XCDs in turn,
+// so each XCD gets a run of the splits' tiles one after the other, and within a
 // split takes columns of up to eight tiles i: what its L2 holds is used by
-// many of its workgroups.
+// many of its workgroups.  A grid smaller than the number of tiles walks its
+// XCD's run.
 struct Tile {
   int i, j, split;
 };
 
-__device__ __forceinline__ Tile tile_of(int i_tiles, int j_tiles) {
-  const int total = (int)gridDim.x, id = (int)blockIdx.x, tiles = i_tiles * j_tiles;
-  const int xcd = id % 8, per = total / 8, more = total % 8;
-  const int at = xcd * per + min(xcd, more) + id / 8;
-  Tile t;
-  t.split = at / tiles;
-  const int in = at - t.split * tiles;
-  const int first = in / (8 * j_tiles) * 8, h = min(8, i_tiles - first);
-  const int k = in - first * j_tiles;
-  t.i = first + k % h;
-  t.j = k / h;
-  return t;
-}
+struct TileWalk {
+  int i_tiles, j_tiles, next, end, stride;
+
+  __device__ __forceinline__ TileWalk(int i_tiles, int j_tiles, int splits)
+      : i_tiles(i_tiles), j_tiles(j_tiles) {
+    const int total = i_tiles * j_tiles * splits, xcd = (int)blockIdx.x % 8;
+    const int per = total / 8, more = total % 8, first = xcd * per + min(xcd, more);
+    next = first + (int)blockIdx.x / 8;
+    end = first + per + (xcd < more ? 1 : 0);
+    stride = ((int)gridDim.x + 7) / 8;
+  }
+
+  // Whether there is one; it is taken.
+  __device__ __forceinline__ bool take(Tile* t) {
+    if (next >= end) return false;
+    const int tiles = i_tiles * j_tiles;
+    t->split = next / tiles;
+    const int in = next - t->split * tiles;
+    const int first = in / (8 * j_tiles) * 8, h = min(8, i_tiles - first);
+    const int k = in - first * j_tiles;
+    t->i = first + k % h;
+    t->j = k / h;
+    next += stride;
+    return true;
+  }
+};
 
 constexpr int kCus = 256;  // compute units
 

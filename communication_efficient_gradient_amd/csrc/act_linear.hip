@@ -43,10 +43,12 @@ struct LinearArgs {
   int mtiles, ntiles;
 };
 
-// A tile of BM tokens by BN outputs per workgroup, WM by WN of it per wave, in
-// k-tiles of BK codes.  An LDS row is BK bytes in CH 16-byte chunks, chunk j of
-// row r at place j ^ (r / (16 / CH) % CH): sixteen lanes that read one chunk of
-// sixteen rows then touch every bank once.
+// Tiles of BM tokens by BN outputs, WM by WN of one per wave, in k-tiles of BK
+// codes.  An LDS row is BK bytes in CH 16-byte chunks, chunk j of row r at
+// place j ^ (r / (16 / CH) % CH): sixteen lanes that read one chunk of sixteen
+// rows then touch every bank once.  Workgroups stay and walk the tiles: the
+// next tile's first k-tile is copied while the present one's last products
+// run, and its copies and products while the results are on their way out.
 template <typename T, int BM, int BN, int WM, int WN, int BK>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(LinearArgs a) {
   constexpr int CH = BK / 16, KK = BK / 32, RPI = 64 / CH;
@@ -57,21 +59,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
-  const Tile tile = tile_of(a.mtiles, a.ntiles);
-  const int64_t m0 = (int64_t)tile.i * BM;
-  const int n0 = tile.j * BN;
-  const int kt0 = tile.split * a.per;
-  const int nk = min(a.per, div_up(a.pitch, BK) - kt0);
 
   // copies: a wave instruction fills RPI rows.  Rows past the end lie behind
   // the buffers' ranges and read as zeros.
   constexpr int CM = BM / RPI / WAVES, CN = BN / RPI / WAVES;
   const int cl = lane % CH, rl = lane / CH;
-  const BufferRange bm = range_of(a.codes + m0 * a.pitch, (a.rows - m0) * a.pitch);
-  const BufferRange bn = range_of(a.w_codes + (int64_t)n0 * a.pitch,
-                                  (int64_t)(a.out - n0) * a.pitch);
+  BufferRange bm, bn;
+  auto ranges_of = [&](const Tile& t) {
+    const int64_t m = (int64_t)t.i * BM, n = (int64_t)t.j * BN;
+    bm = range_of(a.codes + m * a.pitch, (a.rows - m) * a.pitch);
+    bn = range_of(a.w_codes + n * a.pitch, (a.out - n) * a.pitch);
+  };
   auto fill = [&](int kt, int at) {
-    const int k0 = (kt0 + kt) * BK;
+    const int k0 = kt * BK;
     // chunks past the pitch (in the last, short k-tile) are zeros too
     const int left = (a.pitch - k0) / 16;
 #pragma unroll
@@ -87,13 +87,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
                     (LdsPtr)&lds[at + BM * BK + (wave * CN + i) * 1024]);
     }
   };
-  i32x16 acc[NTL][MT];
-#pragma unroll
-  for (int i = 0; i < NTL; ++i)
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
   // The next k-step's fragments (32 rows by 32 codes) are read from LDS between
   // the present one's products (the scheduling groups); the next k-tile is on
@@ -113,105 +106,136 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
     for (int j = 0; j < MT; ++j)
       fm[to][j] = *reinterpret_cast<const i32x4*>(p + (wm + j * 32) * BK);
   };
-  fill(0, 0);
+
+  TileWalk walk(a.mtiles, a.ntiles, a.splits);
+  Tile tile, next;
+  if (!walk.take(&tile)) return;
+  ranges_of(tile);
+  fill(tile.split * a.per, 0);
   __syncthreads();
   read(0, 0, 0);
   int at = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    if (kt + 1 < nk) fill(kt + 1, at ^ BUF);
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      if (kk < KK - 1) {
-        read((kk + 1) & 1, at, kk + 1);
-      } else {
-        __syncthreads();  // the next k-tile is in LDS, this one is read
-        at ^= BUF;
-        read(0, at, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int i = 0; i < NTL; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fn[kk & 1][i], fm[kk & 1][j],
-                                                           acc[i][j], 0, 0, 0);
-#pragma unroll
-      for (int g = 0; g < MT + NTL; ++g) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x008, MT * NTL - MT - NTL, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-  // A lane holds, of one token per 32 x 32 tile, four consecutive outputs in
-  // each of the tile's four quarters: eight bytes of bf16, at 32 rows of y.
-  // The wave's results therefore go through its own part of LDS, TOK tokens
-  // at a time, and leave as whole 16-byte pieces of WN-long rows (measured at
-  // 8192 x 8192 x 4096: 321 us with direct stores).
-  if (a.splits == 1) {
-    using V = typename Word16<T>::V;  // 16 bytes of results
-    constexpr int E = 16 / (int)sizeof(T), ROW = WN / E;  // pieces per row
-    constexpr int TOK = 32 * (2 / ((int)sizeof(T) / 2) < MT ? 2 / ((int)sizeof(T) / 2) : MT);
-    static_assert(TOK * WN * (int)sizeof(T) * WAVES <= (int)sizeof(lds), "");
-    __syncthreads();  // all waves have read their last fragments
-    int8_t* mine = lds + wave * (TOK * WN * (int)sizeof(T));
-    const int lo = lane / 32 * 4;
-#pragma unroll
-    for (int j0 = 0; j0 < MT; j0 += TOK / 32) {
-      float s[TOK / 32];
-#pragma unroll
-      for (int jj = 0; jj < TOK / 32; ++jj)
-        s[jj] = a.steps[min(m0 + wm + (j0 + jj) * 32 + fr, a.rows - 1)];
-#pragma unroll
-      for (int i = 0; i < NTL; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int n = i * 32 + q * 8 + lo;
-          float v[4], b[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int o = min(n0 + wn + n + r, a.out - 1);
-            v[r] = a.w_steps[o];
-            b[r] = a.bias ? a.bias[o] : 0.f;
-          }
-#pragma unroll
-          for (int jj = 0; jj < TOK / 32; ++jj) {
-            const int row = jj * 32 + fr;
-            T o[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              o[r] = (T)((float)acc[i][j0 + jj][q * 4 + r] * s[jj] * v[r] + b[r]);
-            // piece p of row `row` is kept at place p ^ (row % ROW)
-            __builtin_memcpy(
-                mine + (row * ROW + ((n / E) ^ (row % ROW))) * 16 + n % E * (int)sizeof(T), o,
-                sizeof(o));
-          }
-        }
-#pragma unroll
-      for (int k = 0; k < TOK * ROW / 64; ++k) {
-        const int row = (k * 64 + lane) / ROW, p = lane % ROW;
-        const V w = *reinterpret_cast<const V*>(mine + (row * ROW + (p ^ (row % ROW))) * 16);
-        const int64_t m = m0 + wm + j0 * 32 + row;
-        const int n = n0 + wn + p * E;
-        if (m < a.rows) store_piece((T*)a.y + m * a.ldy + n, w, a.out - n);
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int64_t m = m0 + wm + j * 32 + lane % 32;
-    if (m >= a.rows) continue;
+  for (;;) {
+    const int64_t m0 = (int64_t)tile.i * BM;
+    const int n0 = tile.j * BN;
+    const int first = tile.split * a.per, last = min(first + a.per, div_up(a.pitch, BK));
+    const bool more = walk.take(&next);
+    i32x16 acc[NTL][MT];
 #pragma unroll
     for (int i = 0; i < NTL; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + wn + i * 32 + q * 8 + lane / 32 * 4;
-        int32_t* p = a.ws + ((int64_t)tile.split * a.rows + m) * a.out + n;
+      for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (n + r < a.out) p[r] = acc[i][j][q * 4 + r];
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    for (int kt = first; kt < last; ++kt) {
+      if (kt + 1 < last) {
+        fill(kt + 1, at ^ BUF);
+      } else if (more) {
+        ranges_of(next);
+        fill(next.split * a.per, at ^ BUF);
       }
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        if (kk < KK - 1) {
+          read((kk + 1) & 1, at, kk + 1);
+        } else {
+          __syncthreads();  // the next k-tile is in LDS, this one is read
+          at ^= BUF;
+          read(0, at, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int i = 0; i < NTL; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fn[kk & 1][i], fm[kk & 1][j],
+                                                             acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < MT + NTL; ++g) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, MT * NTL - MT - NTL, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // A lane holds, of one token per 32 x 32 tile, four consecutive outputs in
+    // each of the tile's four quarters: eight bytes of bf16, at 32 rows of y.
+    // The wave's results therefore go through its own part of the buffer that
+    // the last k-tile left, TOK tokens at a time, and leave as whole 16-byte
+    // pieces of WN-long rows (8192 x 8192 x 4096: 321 us with direct stores).
+    if (a.splits == 1) {
+      using V = typename Word16<T>::V;  // 16 bytes of results
+      constexpr int E = 16 / (int)sizeof(T), ROW = WN / E;  // pieces per row
+      constexpr int MINE = BUF / WAVES, TOK = MINE / (WN * (int)sizeof(T));
+      static_assert(TOK % 32 == 0 && WM % TOK == 0, "");
+      int8_t* mine = lds + (at ^ BUF) + wave * MINE;
+      const int lo = lane / 32 * 4;
+      const bool whole = n0 + BN <= a.out;
+#pragma unroll
+      for (int j0 = 0; j0 < MT; j0 += TOK / 32) {
+        float s[TOK / 32];
+#pragma unroll
+        for (int jj = 0; jj < TOK / 32; ++jj)
+          s[jj] = a.steps[min(m0 + wm + (j0 + jj) * 32 + fr, a.rows - 1)];
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = i * 32 + q * 8 + lo;
+            float v[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+            if (whole) {
+              __builtin_memcpy(v, a.w_steps + n0 + wn + n, 16);
+              if (a.bias) __builtin_memcpy(b, a.bias + n0 + wn + n, 16);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int o = min(n0 + wn + n + r, a.out - 1);
+                v[r] = a.w_steps[o];
+                if (a.bias) b[r] = a.bias[o];
+              }
+            }
+#pragma unroll
+            for (int jj = 0; jj < TOK / 32; ++jj) {
+              const int row = jj * 32 + fr;
+              T o[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                o[r] = (T)((float)acc[i][j0 + jj][q * 4 + r] * s[jj] * v[r] + b[r]);
+              // piece p of row `row` is kept at place p ^ (row % ROW)
+              __builtin_memcpy(
+                  mine + (row * ROW + ((n / E) ^ (row % ROW))) * 16 + n % E * (int)sizeof(T),
+                  o, sizeof(o));
+            }
+          }
+#pragma unroll
+        for (int k = 0; k < TOK * ROW / 64; ++k) {
+          const int row = (k * 64 + lane) / ROW, p = lane % ROW;
+          const V w = *reinterpret_cast<const V*>(mine + (row * ROW + (p ^ (row % ROW))) * 16);
+          const int64_t m = m0 + wm + j0 * 32 + row;
+          const int n = n0 + wn + p * E;
+          if (m < a.rows) store_piece((T*)a.y + m * a.ldy + n, w, a.out - n);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const int64_t m = m0 + wm + j * 32 + lane % 32;
+        if (m >= a.rows) continue;
+#pragma unroll
+        for (int i = 0; i < NTL; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int n = n0 + wn + i * 32 + q * 8 + lane / 32 * 4;
+            int32_t* p = a.ws + ((int64_t)tile.split * a.rows + m) * a.out + n;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (n + r < a.out) p[r] = acc[i][j][q * 4 + r];
+          }
+      }
+    }
+    if (!more) return;
+    tile = next;
+    __syncthreads();  // all waves are done with the buffer that is filled next
   }
 }
 
@@ -372,7 +396,9 @@ int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
   }
   a.mtiles = div_up(A.rows, tile);
   a.ntiles = div_up(a.out, tile);
-  const unsigned g = (unsigned)(a.mtiles * a.ntiles * a.splits);
+  const int64_t tiles = (int64_t)a.mtiles * a.ntiles * a.splits;
+  const int64_t most = tile == 256 ? kCus : 2 * kCus;  // what the chip holds
+  const unsigned g = (unsigned)(tiles < most ? tiles : most);
   if (tile == 256) k_act_linear<T, 256, 256, 128, 64, 128><<<g, 512, 0, st>>>(a);
   else k_act_linear<T, 128, 128, 64, 64, 128><<<g, 256, 0, st>>>(a);
   int rc = (int)hipGetLastError();

@@ -113,7 +113,8 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wo = wave % (BO / WO) * WO, wc = wave / (BO / WO) * WC;
-  const Tile tile = tile_of(a.otiles, a.ctiles);
+  Tile tile;
+  if (!TileWalk(a.otiles, a.ctiles, a.splits).take(&tile)) return;
   const int ot = tile.i, ct = tile.j;
   const int o0 = ot * BO, c0 = ct * BC;
   const int64_t t0 = (int64_t)tile.split * a.per;
