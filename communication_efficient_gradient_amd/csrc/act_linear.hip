@@ -368,21 +368,39 @@ void few(const LinearArgs& a, hipStream_t st) {
 }
 
 struct Plan {
-  int splits, per;
-  int tile;  // rows and columns of a tile
+  int splits, per;  // of the sum, and 128-byte k-tiles of one
+  int tile;         // rows and columns of a tile
 };
 
+// The tile's side and the number of splits by an estimate of the time in
+// microseconds: rounds of tiles (one 256 x 256 or two 128 x 128 per CU), a
+// k-tile each, what a tile costs besides, and the splits' sums through memory.
+// Measured (tokens x out x cols): 4096 x 4096 x 4096 65 us with 256-tiles, 75
+// with 128; 1024 x 4096 x 4096 43 and 29, 2000 x 4000 x 1000 23 and 18; two
+// splits only pay for long sums on few tiles (8192 x 512 x 8192: 50 us
+// unsplit, 68 with two; 512 x 4096 x 4096 27 and 35).
 Plan plan_linear(const ActDims& A, int64_t out) {
   const int kt = div_up(A.pitch, 128);
-  Plan p = {1, kt, 0};
-  if (few_tokens(A, out)) return p;
-  p.tile = ((A.rows + 255) / 256) * ((out + 255) / 256) >= 128 ? 256 : 128;
-  const int64_t tiles = ((A.rows + p.tile - 1) / p.tile) * ((out + p.tile - 1) / p.tile);
-  int splits = tiles >= kCus ? 1 : (int)(kCus / tiles);
-  if (splits > kt / 4) splits = kt / 4 > 0 ? kt / 4 : 1;
-  p.per = div_up(kt, splits);
-  p.splits = div_up(kt, p.per);
-  return p;
+  Plan best = {1, kt, 0};
+  if (few_tokens(A, out)) return best;
+  double least = 1e30;
+  for (int tile = 128; tile <= 256; tile *= 2) {
+    const int64_t tiles = ((A.rows + tile - 1) / tile) * ((out + tile - 1) / tile);
+    for (int s = 1; s <= 8 && (s == 1 || kt / s >= 8); ++s) {
+      const int per = div_up(kt, s);
+      const int64_t groups = tiles * s;
+      double t;
+      if (tile == 256) t = (double)((groups + kCus - 1) / kCus) * (per * 1.6 + 12.0);
+      else if (groups <= kCus) t = per * 0.72 + 5.0;
+      else t = (double)((groups + 2 * kCus - 1) / (2 * kCus)) * (per * 1.15 + 8.0);
+      if (s > 1) t += 10.0 + 8.0 * (double)(s * A.rows) * (double)out / 2.4e6;
+      if (t < least) {
+        least = t;
+        best = {div_up(kt, per), per, tile};
+      }
+    }
+  }
+  return best;
 }
 
 template <typename T>

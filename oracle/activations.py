@@ -53,7 +53,8 @@ def unpack(codes: np.ndarray, steps: np.ndarray, cols: int, group: int = 0) -> n
 
 
 def linear(codes, steps, w_codes, w_steps, bias, cols: int) -> np.ndarray:
-    acc = codes[:, :cols].astype(np.int64) @ w_codes[:, :cols].astype(np.int64).T
+    # whole numbers below 2^53: exact in 64-bit floats
+    acc = codes[:, :cols].astype(np.float64) @ w_codes[:, :cols].astype(np.float64).T
     y = acc * steps.reshape(-1, 1).astype(np.float64) * w_steps.astype(np.float64)[None, :]
     return y if bias is None else y + bias.astype(np.float64)
 

@@ -96,14 +96,15 @@ def test_linear_refusals(gq):
     assert call(ld=49) == -1
     assert call(y=3 * M) == -1                         # over the weight
     assert call(y=5 * M + 196) == -1                   # over the bias's last value
-    big = dict(desc=act(gq, rows=1200, cols=4096), out=1200, ld=1200)
+    big = dict(desc=act(gq, rows=1100, cols=60000), out=1000, ld=1000, codes=M, steps=8 * M,
+               wc=9 * M, ws=14 * M, bias=15 * M, y=16 * M, work=17 * M)
     need = C.c_int64()
-    assert L.gq_act_linear_workspace(C.byref(big["desc"]), 1200, C.byref(need)) == 0
+    assert L.gq_act_linear_workspace(C.byref(big["desc"]), 1000, C.byref(need)) == 0
     assert need.value > 0
     assert call(**big, nb=need.value - 1) == -1
-    assert call(**big, work=None) == -1
-    assert call(**big, work=7 * M + 8) == -1
-    assert call(**big, work=M) == -1                   # over the codes
+    assert call(**{**big, "work": None}) == -1
+    assert call(**{**big, "work": 17 * M + 8}) == -1
+    assert call(**{**big, "work": M}) == -1            # over the codes
     assert call(desc=act(gq, rows=0), codes=None, steps=None, y=None) == 0
 
 

@@ -72,6 +72,14 @@ def test_large_tiles(gq):
     check(gq, 2500, 2500, 129, "f32")
 
 
+def test_long_sums_are_split(gq):
+    """Few tiles and a long sum: split and joined."""
+    a = gq.act(1111, 16000, torch.bfloat16)
+    assert gq.gq_act_linear_workspace(a, 1000) > 0
+    check(gq, 1111, 1000, 16000, "bf16", pad=3, lead=1)
+    check(gq, 1100, 1001, 15001, "f32", bias=False)
+
+
 @pytest.mark.parametrize("rows", [1, 40, 300])
 def test_extreme_codes(gq, rows):
     """All codes at the ends, over the longest sum that 32 bits hold."""
