@@ -46,16 +46,17 @@ struct LinearArgs {
 // Tiles of BM tokens by BN outputs, WM by WN of one per wave, in k-tiles of BK
 // codes.  An LDS row is BK bytes in CH 16-byte chunks, chunk j of row r at
 // place j ^ (r / (16 / CH) % CH): sixteen lanes that read one chunk of sixteen
-// rows then touch every bank once.  Workgroups stay and walk the tiles: the
-// next tile's first k-tile is copied while the present one's last products
-// run, and its copies and products while the results are on their way out.
-template <typename T, int BM, int BN, int WM, int WN, int BK>
+// rows then touch every bank once.  NS k-tiles share LDS: one is multiplied
+// while NS - 1 are on their way.  Workgroups stay and walk the tiles, and the
+// copies run on into the next tile while the present one's last products run
+// and its results leave.
+template <typename T, int BM, int BN, int WM, int WN, int BK, int NS>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(LinearArgs a) {
   constexpr int CH = BK / 16, KK = BK / 32, RPI = 64 / CH;
   constexpr int WAVES = (BM / WM) * (BN / WN);
   constexpr int MT = WM / 32, NTL = WN / 32;
   constexpr int BUF = (BM + BN) * BK;
-  __shared__ __attribute__((aligned(16))) int8_t lds[2 * BUF];
+  __shared__ __attribute__((aligned(16))) int8_t lds[NS * BUF];
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
@@ -70,22 +71,53 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
     bm = range_of(a.codes + m * a.pitch, (a.rows - m) * a.pitch);
     bn = range_of(a.w_codes + n * a.pitch, (a.out - n) * a.pitch);
   };
-  auto fill = [&](int kt, int at) {
-    const int k0 = kt * BK;
+  const int k_tiles = div_up(a.pitch, BK);
+  // what is copied next: k-tile ck (up to cend) of the walk's last tile, into cat
+  TileWalk copies(a.mtiles, a.ntiles, a.splits);
+  Tile ctile;
+  bool copying = copies.take(&ctile);
+  int ck = 0, cend = 0, cat = 0;
+  auto enter = [&] {
+    ranges_of(ctile);
+    ck = ctile.split * a.per;
+    cend = min(ck + a.per, k_tiles);
+  };
+  auto copy_next = [&] {
+    if (!copying) return;
+    const int k0 = ck * BK;
     // chunks past the pitch (in the last, short k-tile) are zeros too
     const int left = (a.pitch - k0) / 16;
 #pragma unroll
     for (int i = 0; i < CM; ++i) {
       const int r = (wave * CM + i) * RPI + rl, c = cl ^ (r / (16 / CH) % CH);
       copy16_to_lds(bm, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
-                    (LdsPtr)&lds[at + (wave * CM + i) * 1024]);
+                    (LdsPtr)&lds[cat + (wave * CM + i) * 1024]);
     }
 #pragma unroll
     for (int i = 0; i < CN; ++i) {
       const int r = (wave * CN + i) * RPI + rl, c = cl ^ (r / (16 / CH) % CH);
       copy16_to_lds(bn, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
-                    (LdsPtr)&lds[at + BM * BK + (wave * CN + i) * 1024]);
+                    (LdsPtr)&lds[cat + BM * BK + (wave * CN + i) * 1024]);
     }
+    cat = cat + BUF == NS * BUF ? 0 : cat + BUF;
+    if (++ck == cend) {
+      copying = copies.take(&ctile);
+      if (copying) enter();
+    }
+  };
+  // Waits until this wave's reads are done and its copies but those of the NS -
+  // 2 youngest k-tiles have arrived, then for the other waves.  Copies arrive
+  // in order; anything else in flight (results on their way out) only makes
+  // the wait longer.  Once there is nothing left to copy the youngest are
+  // fewer, so all are waited for.
+  auto meet = [&](bool all) {
+    if (NS == 2 || all) {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * (CM + CN)) : "memory");
+    }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
 
   // The next k-step's fragments (32 rows by 32 codes) are read from LDS between
@@ -108,18 +140,18 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
   };
 
   TileWalk walk(a.mtiles, a.ntiles, a.splits);
-  Tile tile, next;
+  Tile tile;
   if (!walk.take(&tile)) return;
-  ranges_of(tile);
-  fill(tile.split * a.per, 0);
-  __syncthreads();
+  enter();
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy_next();
+  meet(!copying);
   read(0, 0, 0);
   int at = 0;
   for (;;) {
     const int64_t m0 = (int64_t)tile.i * BM;
     const int n0 = tile.j * BN;
-    const int first = tile.split * a.per, last = min(first + a.per, div_up(a.pitch, BK));
-    const bool more = walk.take(&next);
+    const int first = tile.split * a.per, last = min(first + a.per, k_tiles);
     i32x16 acc[NTL][MT];
 #pragma unroll
     for (int i = 0; i < NTL; ++i)
@@ -127,20 +159,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
       for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    int was = at;
     for (int kt = first; kt < last; ++kt) {
-      if (kt + 1 < last) {
-        fill(kt + 1, at ^ BUF);
-      } else if (more) {
-        ranges_of(next);
-        fill(next.split * a.per, at ^ BUF);
-      }
+      was = at;
+      copy_next();
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
         if (kk < KK - 1) {
           read((kk + 1) & 1, at, kk + 1);
         } else {
-          __syncthreads();  // the next k-tile is in LDS, this one is read
-          at ^= BUF;
+          meet(!copying);  // the next k-tile is in LDS, this one is read
+          at = at + BUF == NS * BUF ? 0 : at + BUF;
           read(0, at, 0);
         }
 #pragma unroll
@@ -154,7 +183,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, MT * NTL - MT - NTL, 0);
+        if (MT * NTL > MT + NTL)
+          __builtin_amdgcn_sched_group_barrier(0x008, MT * NTL - MT - NTL, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -166,9 +196,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
     if (a.splits == 1) {
       using V = typename Word16<T>::V;  // 16 bytes of results
       constexpr int E = 16 / (int)sizeof(T), ROW = WN / E;  // pieces per row
-      constexpr int MINE = BUF / WAVES, TOK = MINE / (WN * (int)sizeof(T));
+      constexpr int MINE = BUF / WAVES, FIT = MINE / (WN * (int)sizeof(T));
+      constexpr int TOK = FIT < WM ? FIT : WM;
       static_assert(TOK % 32 == 0 && WM % TOK == 0, "");
-      int8_t* mine = lds + (at ^ BUF) + wave * MINE;
+      int8_t* mine = lds + was + wave * MINE;
       const int lo = lane / 32 * 4;
       const bool whole = n0 + BN <= a.out;
 #pragma unroll
@@ -233,9 +264,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
           }
       }
     }
-    if (!more) return;
-    tile = next;
-    __syncthreads();  // all waves are done with the buffer that is filled next
+    if (!walk.take(&tile)) return;
+    // all waves are done with the buffer that is filled next
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
 }
 
@@ -351,15 +384,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_act_linear_few(LinearArgs a)
   }
 }
 
-// Up to 512 of the small tiles (64 tokens by 32 outputs: two a CU) the tiled
-// kernel's barriers and the join of its splits cost more than operands read
-// oftener.  Measured, small against tiled: 128 x 4096 x 4096 (tokens x out x
-// cols) 17 and 27 us, 203 x 2050 x 4100 20 and 25, 300 x 1024 x 1024 8.5 and
-// 16, 256 x 4096 x 4096 27 and 29.5; with 1024 tiles, 512 x 4096 x 4096, 49
-// and 34 us.
-bool few_tokens(const ActDims& A, int64_t out) {
-  return A.rows <= 64 || ((A.rows + 63) / 64) * ((out + 31) / 32) <= 512;
-}
+// From 65 tokens on the tiled kernel is faster (64 x 4096 x 4096, tokens x out
+// x cols: 11 us here, 15 there; 203 x 2050 x 4100: 20 and 15).
+bool few_tokens(const ActDims& A) { return A.rows <= 64; }
 
 template <typename T, int MT, int NT, int U>
 void few(const LinearArgs& a, hipStream_t st) {
@@ -373,26 +400,29 @@ struct Plan {
 };
 
 // The tile's side and the number of splits by an estimate of the time in
-// microseconds: rounds of tiles (one 256 x 256 or two 128 x 128 per CU), a
-// k-tile each, what a tile costs besides, and the splits' sums through memory.
-// Measured (tokens x out x cols): 4096 x 4096 x 4096 65 us with 256-tiles, 75
-// with 128; 1024 x 4096 x 4096 43 and 29, 2000 x 4000 x 1000 23 and 18; two
-// splits only pay for long sums on few tiles (8192 x 512 x 8192: 50 us
-// unsplit, 68 with two; 512 x 4096 x 4096 27 and 35).
+// microseconds: rounds of tiles over the chip, their k-tiles, what a tile costs
+// besides, and the splits' sums through memory.  Measured (tokens x out x
+// cols): 4096 x 4096 x 4096 63 us with 256-tiles, 75 with 128; 1024 x 4096 x
+// 4096 25 us with 128-tiles, 36 with 64, 43 with 256; 512 x 4096 x 4096 18 us
+// with 64, 20 with 128; two splits only pay for long sums on few tiles (8192 x
+// 512 x 8192: 50 us unsplit, 68 with two, both with the 128-tiles of two
+// k-tiles in LDS that take 42 now with four).
 Plan plan_linear(const ActDims& A, int64_t out) {
   const int kt = div_up(A.pitch, 128);
   Plan best = {1, kt, 0};
-  if (few_tokens(A, out)) return best;
+  if (few_tokens(A)) return best;
   double least = 1e30;
-  for (int tile = 128; tile <= 256; tile *= 2) {
+  for (int tile = 64; tile <= 256; tile *= 2) {
     const int64_t tiles = ((A.rows + tile - 1) / tile) * ((out + tile - 1) / tile);
     for (int s = 1; s <= 8 && (s == 1 || kt / s >= 8); ++s) {
       const int per = div_up(kt, s);
       const int64_t groups = tiles * s;
+      const double rounds = (double)((groups + kCus - 1) / kCus);
       double t;
-      if (tile == 256) t = (double)((groups + kCus - 1) / kCus) * (per * 1.6 + 12.0);
-      else if (groups <= kCus) t = per * 0.72 + 5.0;
-      else t = (double)((groups + 2 * kCus - 1) / (2 * kCus)) * (per * 1.15 + 8.0);
+      if (tile == 256) t = rounds * (per * 1.6 + 12.0);
+      else if (tile == 128) t = rounds * (per * 0.6 + 5.0);
+      else if (groups <= kCus) t = per * 0.33 + 4.0;
+      else t = (double)((groups + 2 * kCus - 1) / (2 * kCus)) * (per * 0.44 + 4.0);
       if (s > 1) t += 10.0 + 8.0 * (double)(s * A.rows) * (double)out / 2.4e6;
       if (t < least) {
         least = t;
@@ -405,20 +435,20 @@ Plan plan_linear(const ActDims& A, int64_t out) {
 
 template <typename T>
 int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
-  if (few_tokens(A, a.out)) {
+  if (few_tokens(A)) {
     if (A.rows <= 16) few<T, 1, 1, 8>(a, st);
     else if (A.rows <= 32) few<T, 2, 1, 4>(a, st);
-    else if (A.rows <= 64) few<T, 2, 2, 4>(a, st);
-    else few<T, 4, 2, 2>(a, st);
+    else few<T, 2, 2, 4>(a, st);
     return (int)hipGetLastError();
   }
   a.mtiles = div_up(A.rows, tile);
   a.ntiles = div_up(a.out, tile);
   const int64_t tiles = (int64_t)a.mtiles * a.ntiles * a.splits;
-  const int64_t most = tile == 256 ? kCus : 2 * kCus;  // what the chip holds
+  const int64_t most = tile == 64 ? 2 * kCus : kCus;  // what the chip holds
   const unsigned g = (unsigned)(tiles < most ? tiles : most);
-  if (tile == 256) k_act_linear<T, 256, 256, 128, 64, 128><<<g, 512, 0, st>>>(a);
-  else k_act_linear<T, 128, 128, 64, 64, 128><<<g, 256, 0, st>>>(a);
+  if (tile == 256) k_act_linear<T, 256, 256, 128, 64, 128, 2><<<g, 512, 0, st>>>(a);
+  else if (tile == 128) k_act_linear<T, 128, 128, 64, 32, 128, 4><<<g, 512, 0, st>>>(a);
+  else k_act_linear<T, 64, 64, 32, 32, 128, 4><<<g, 256, 0, st>>>(a);
   int rc = (int)hipGetLastError();
   if (rc == 0 && a.splits > 1) {
     const int64_t b = (A.rows * a.out + 255) / 256;
