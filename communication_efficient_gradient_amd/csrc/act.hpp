@@ -239,7 +239,8 @@ __device__ __forceinline__ BufferRange range_of(const void* base, int64_t bytes)
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
 }
 
-constexpr int kPastEnd = (int)0x80000000;  // an offset no range used here has
+// An offset behind the end of any range below 2 GiB.
+constexpr int kPastEnd = (int)0x80000000;
 
 // 16 bytes per lane into LDS at `to` (the same in all lanes) + 16 * lane,
 // without passing through registers; `each` differs by lane, `all` does not.

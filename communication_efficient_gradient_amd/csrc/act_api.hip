@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxElements = int64_t(1) << 38;
 constexpr int64_t kMaxCols = int64_t(1) << 20;
 constexpr int64_t kMaxLinearCols = 131071;  // 2^7 * 2^7 * cols < 2^31
+constexpr int64_t kMaxTiles = int64_t(1) << 24;  // of 64 x 64 results
 
 bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
@@ -43,6 +44,13 @@ int check_act(const gq_act* a, gq::ActDims* A) {
 int check_out(const gq::ActDims& A, int64_t out) {
   if (out < 1 || out > kMaxCols) return GQ_EINVAL;
   if (A.rows > kMaxElements / out || out > kMaxElements / A.cols) return GQ_EINVAL;
+  return GQ_OK;
+}
+
+// One step per row, sums that 32 bits hold, tiles that one launch numbers.
+int check_linear(const gq::ActDims& A, int64_t out) {
+  if (!A.whole_row || A.cols > kMaxLinearCols) return GQ_EUNSUPPORTED;
+  if ((A.rows + 63) / 64 > kMaxTiles / ((out + 63) / 64)) return GQ_EUNSUPPORTED;
   return GQ_OK;
 }
 
@@ -148,7 +156,8 @@ int gq_act_linear_workspace(const gq_act* act, int64_t out, int64_t* bytes) {
   if (rc == GQ_OK) rc = check_out(A, out);
   if (rc) return rc;
   if (!bytes) return GQ_EINVAL;
-  if (!A.whole_row || A.cols > kMaxLinearCols) return GQ_EUNSUPPORTED;
+  rc = check_linear(A, out);
+  if (rc) return rc;
   *bytes = gq::act_linear_workspace(A, out);
   return GQ_OK;
 }
@@ -161,8 +170,8 @@ int gq_act_linear(const gq_act* act, int64_t out, const int8_t* codes,
   gq::ActDims A;
   int rc = check_act(act, &A);
   if (rc == GQ_OK) rc = check_out(A, out);
+  if (rc == GQ_OK) rc = check_linear(A, out);
   if (rc) return rc;
-  if (!A.whole_row || A.cols > kMaxLinearCols) return GQ_EUNSUPPORTED;
   Range ry, rc8, rs;
   if (!matrix(A, y, out, ldy, &ry) || !form(A, codes, steps, &rc8, &rs))
     return GQ_EINVAL;

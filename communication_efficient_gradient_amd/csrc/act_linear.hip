@@ -68,8 +68,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_act_linear(Li
   BufferRange bm, bn;
   auto ranges_of = [&](const Tile& t) {
     const int64_t m = (int64_t)t.i * BM, n = (int64_t)t.j * BN;
-    bm = range_of(a.codes + m * a.pitch, (a.rows - m) * a.pitch);
-    bn = range_of(a.w_codes + n * a.pitch, (a.out - n) * a.pitch);
+    // of this tile's rows only: shorter than kPastEnd whatever the matrix
+    bm = range_of(a.codes + m * a.pitch, min(a.rows - m, (int64_t)BM) * a.pitch);
+    bn = range_of(a.w_codes + n * a.pitch, min(a.out - n, (int64_t)BN) * a.pitch);
   };
   const int k_tiles = div_up(a.pitch, BK);
   // what is copied next: k-tile ck (up to cend) of the walk's last tile, into cat
@@ -304,8 +305,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_act_linear_few(LinearArgs a)
   const int n0 = (int)blockIdx.x * (16 * NT);
   const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
   const BufferRange w = range_of(a.w_codes + (int64_t)n0 * a.pitch,
-                                 (int64_t)(a.out - n0) * a.pitch);
-  const BufferRange x = range_of(a.codes + m0 * a.pitch, (a.rows - m0) * a.pitch);
+                                 (int64_t)min(a.out - n0, 16 * NT) * a.pitch);
+  const BufferRange x = range_of(a.codes + m0 * a.pitch,
+                                 min(a.rows - m0, (int64_t)(16 * MT)) * a.pitch);
   const int row = lane % 16 * a.pitch, col = lane / 16 * 16;
   i32x4 acc[NT][MT];
 #pragma unroll

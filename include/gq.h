@@ -386,7 +386,8 @@ int gq_act_unpack(const gq_act* act, const int8_t* codes, const float* steps,
  *             + bias[o]
  * The integer sum is exact; the rest is fp32, rounded once to act's type.
  * codes, steps: the 8-bit form of the layer's input with one step per row
- * (GQ_EUNSUPPORTED for act->group != 0 and for cols > 131071).  w_codes,
+ * (GQ_EUNSUPPORTED for act->group != 0, for cols > 131071 and for more than
+ * 2^24 tiles of 64 x 64 results).  w_codes,
  * w_steps: the weight [out, cols] in the same layout, one step per output
  * feature; these may also come from elsewhere: any codes -128 .. 127 (0 past
  * the last column) and any fp32 steps.  bias fp32 [out] or NULL.  workspace:

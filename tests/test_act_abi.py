@@ -86,6 +86,7 @@ def test_linear_refusals(gq):
     assert call(out=0) == -1
     assert call(desc=act(gq, group=32)) == -2          # one step per row only
     assert call(desc=act(gq, cols=131072)) == -2       # the sum would not fit 32 bits
+    assert call(desc=act(gq, rows=1 << 31, cols=1), out=64, nb=1 << 40) == -2  # too many tiles
     assert call(codes=None) == -1
     assert call(steps=None) == -1
     assert call(wc=None) == -1

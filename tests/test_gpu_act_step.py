@@ -213,23 +213,48 @@ def test_offsets_past_32_bits(gq):
                                atol=4.5 * 2 ** -8 * 2)
 
 
-def test_integer_product_past_32_bits(gq):
-    rows, cols, out = 270_000, 8192, 24
+@pytest.mark.parametrize("rows,cols,out", [(270_000, 8192, 24), (270_000, 8200, 24),
+                                           (600_000, 8200, 70)])
+def test_integer_product_past_32_bits(gq, rows, cols, out):
+    """Also with a last k-tile that is short: what lies behind its end is not
+    the codes two gigabytes further."""
     a = gq.act(rows, cols, torch.bfloat16)
     assert rows * a.pitch > 2 ** 31
     codes, steps = gq.alloc_act(a)
-    codes.zero_()
+    codes.fill_(1)
+    codes[:, cols:] = 0
     steps.fill_(0.5)
     rng = np.random.default_rng(11)
-    last = rng.integers(-127, 128, (2, cols)).astype(np.int8)
+    last = rng.integers(-127, 128, (2, a.pitch)).astype(np.int8)
+    last[:, cols:] = 0
     codes[-2:] = torch.as_tensor(last).cuda()
-    w = rng.integers(-127, 128, (out, cols)).astype(np.int8)
+    w = rng.integers(-127, 128, (out, a.pitch)).astype(np.int8)
+    w[:, cols:] = 0
     y = torch.full((rows, out), 9.0, dtype=torch.bfloat16, device="cuda")
     work = gq.alloc_workspace(gq.gq_act_linear_workspace(a, out))
     gq.gq_act_linear(a, codes, steps, torch.as_tensor(w).cuda(), torch.ones(out, device="cuda"),
                      None, y, workspace=work)
-    want = A.linear(last, np.full((2, 1), 0.5, np.float32), w, np.ones(out, np.float32), None,
-                    cols)
+    half, one = np.full((2, 1), 0.5, np.float32), np.ones(out, np.float32)
+    want = A.linear(last, half, w, one, None, cols)
     got = y[-2:].double().cpu().numpy()
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want)).all()
-    assert (y[:-2] == 0).all()
+    rest = A.linear(np.ones((1, cols), np.int8), half[:1], w, one, None, cols)
+    assert torch.equal(y[:-2], torch.as_tensor(rest).bfloat16().cuda().expand(rows - 2, out))
+
+
+def test_few_tokens_through_a_weight_past_32_bits(gq):
+    out, cols = 270_000, 8200
+    a, aw = gq.act(3, cols, torch.float32), gq.act(out, cols, torch.float32)
+    w, v = gq.alloc_act(aw)
+    assert w.numel() > 2 ** 31
+    w.fill_(1)
+    w[:, cols:] = 0
+    v.fill_(1.0)
+    x, s = gq.alloc_act(a)
+    x.fill_(2)
+    x[:, cols:] = 0
+    s.fill_(1.0)
+    w[-1, :cols] = 3
+    y = torch.zeros(3, out, device="cuda")
+    gq.gq_act_linear(a, x, s, w, v.view(-1), None, y)
+    assert (y[:, :-1] == 2 * cols).all() and (y[:, -1] == 6 * cols).all()
