@@ -84,35 +84,48 @@ __device__ __forceinline__ void shift_down(Raw8<T>& r, int n) {
   }
 }
 
+// How a row ends.  kWhole: cols % 8 == 0, a chunk is the row's or past its end
+// as a whole.  kRagged: the last chunk is short.  It is fetched as the row's
+// last eight values, in the same instruction as the other lanes' chunks, and
+// settle() moves it down where it is used.  kTiny: fewer than eight columns,
+// read by elements.  A way through elements, or moving the values where they
+// are loaded, makes loads of the wave wait for those before (backward pass of
+// 1531 x 1001 fp16: 8.9 us with both in the kernel, 7.9 so; layer norm of 16384
+// x 4096 bf16 with its input's 8-bit form: 93 us through elements, 68 with whole
+// chunks).
+enum RowEnd { kWhole = 0, kRagged = 1, kTiny = 2 };
+
+inline RowEnd row_end(int64_t cols) {
+  return cols % 8 == 0 ? kWhole : cols >= 8 ? kRagged : kTiny;
+}
+
 // Columns c .. c + 7 of a row that ends before column `end`; what lies past it
-// is 0.  RAGGED (cols % 8 != 0): the last chunk of a row is short.  It is
-// fetched as the row's last eight values and moved down, in the same
-// instruction as the other lanes' chunks; through single elements every load
-// of the wave waited for it (layer norm of 16384 x 4096 bf16 with its input's
-// 8-bit form: 93 us when all rows took that way, 68 with whole chunks;
-// backward from the form 117 and 73).  Rows shorter than a chunk are read by
-// elements.
-template <bool RAGGED, typename T>
+// is 0 (kRagged: once settled).
+template <int END, typename T>
 __device__ __forceinline__ Raw8<T> load_chunk(const T* __restrict__ row, int c, int end) {
   Raw8<T> r = {};
   const int valid = end - c;
-  if constexpr (!RAGGED) {
+  if constexpr (END == kWhole) {
     if (valid > 0) __builtin_memcpy(&r, row + c, sizeof(r));
-  } else if (c < 8 && valid < 8) {
+  } else if constexpr (END == kRagged) {
+    if (valid > 0) __builtin_memcpy(&r, row + min(c, end - 8), sizeof(r));
+  } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < valid) r.v[j] = row[c + j];
-  } else {
-    const int back = valid > 0 && valid < 8 ? 8 - valid : 0;
-    if (valid > 0) __builtin_memcpy(&r, row + c - back, sizeof(r));
-    if (back) shift_down(r, back);
   }
   return r;
 }
 
-template <bool RAGGED, typename T>
+template <int END, typename T>
+__device__ __forceinline__ void settle(Raw8<T>& r, int c, int end) {
+  const int valid = end - c;
+  if (END == kRagged && valid > 0 && valid < 8) shift_down(r, 8 - valid);
+}
+
+template <int END, typename T>
 __device__ __forceinline__ void store_chunk(T* p, const Raw8<T>& r, int valid) {
-  if (RAGGED) return store8(p, r, valid);
+  if (END != kWhole) return store8(p, r, valid);
   if (valid > 0) __builtin_memcpy(p, &r, sizeof(r));
 }
 

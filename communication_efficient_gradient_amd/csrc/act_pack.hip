@@ -45,7 +45,7 @@ __device__ __forceinline__ void next_unit(Unit* u, int turns) {
 }
 
 // Groups of G * 8 columns, G = 4..64 lanes.
-template <typename T, bool RAGGED>
+template <typename T, int END>
 __global__ __launch_bounds__(kBlock) void k_act_pack_lanes(
     int64_t rows, int cols, int pitch, int groups, int Glog, int turns, int tlog,
     const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
@@ -59,13 +59,14 @@ __global__ __launch_bounds__(kBlock) void k_act_pack_lanes(
   for (int i = 0; i < UNITS; ++i, next_unit(&u, turns)) {
     const int64_t row = u.rows0 * per + in;
     const int c = (u.turn * tpr + lane) * 8;
-    raw[i] = load_chunk<RAGGED>(x + row * ldx, c, row < rows ? cols : 0);
+    raw[i] = load_chunk<END>(x + row * ldx, c, row < rows ? cols : 0);
   }
 #pragma unroll
   for (int i = 0; i < UNITS; ++i, next_unit(&v, turns)) {
     const int64_t row = v.rows0 * per + in;
     const int c = v.turn * tpr + lane;
     float f[8];
+    settle<END>(raw[i], c * 8, row < rows ? cols : 0);
     widen(raw[i], f);
     const Step s = step_of<T>(lanes_max(max_abs_bits(f), G));
     if (row < rows) {
@@ -93,7 +94,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
 
 // One group (a whole row, or 1024 columns and more) per NT threads: R chunks
 // of each thread stay in registers; R = 0 reads the group twice.
-template <typename T, int NT, int R, bool RAGGED>
+template <typename T, int NT, int R, int END>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
     int64_t rows, int cols, int pitch, int groups, int group,
     const T* __restrict__ x, int64_t ldx, int8_t* __restrict__ codes,
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (lane + i * NT) * 8;
-      raw[i] = load_chunk<RAGGED>(x + row * ldx, lo + c, s < total ? lo + n : 0);
+      raw[i] = load_chunk<END>(x + row * ldx, lo + c, s < total ? lo + n : 0);
     }
   };
   if constexpr (R > 0) fetch(at);
@@ -128,6 +129,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
       float f[R][8];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
+        settle<END>(raw[i], lo + (lane + i * NT) * 8, lo + n);
         widen(raw[i], f[i]);
         m = max(m, max_abs_bits(f[i]));
       }
@@ -156,7 +158,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_act_pack_seg(
   }
 }
 
-template <typename T, bool RAGGED>
+template <typename T, int END>
 __global__ __launch_bounds__(kBlock) void k_act_unpack(
     int64_t rows, int cols, int pitch, int groups, int glog, int turns, int tlog,
     const int8_t* __restrict__ codes, const float* __restrict__ steps,
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(kBlock) void k_act_unpack(
     const int c = (v.turn * tpr + lane) * 8;
     float f[8];
     decode8(w[i], s[i], f);
-    store_chunk<RAGGED>(x + row * ldx + c, narrow<T>(f), row < rows ? cols - c : 0);
+    store_chunk<END>(x + row * ldx + c, narrow<T>(f), row < rows ? cols - c : 0);
   }
 }
 
@@ -227,7 +229,9 @@ void pack_seg(const ActDims& A, const T* x, int64_t ldx, int8_t* codes,
   constexpr int BT = NT < 256 ? 256 : NT;
   // resident workgroups, each thread with the next group on its way
   const unsigned g = blocks_for(A.rows * A.groups, BT / NT, kCus * (2048 / BT));
-  auto* k = A.cols % 8 ? k_act_pack_seg<T, NT, R, true> : k_act_pack_seg<T, NT, R, false>;
+  auto* k = A.cols % 8 ? k_act_pack_seg<T, NT, R, kRagged> : k_act_pack_seg<T, NT, R, kWhole>;
+  if constexpr (NT == 64 && R == 1)
+    if (row_end(A.cols) == kTiny) k = k_act_pack_seg<T, NT, R, kTiny>;
   k<<<g, BT, 0, st>>>(
       A.rows, (int)A.cols, (int)A.pitch, A.groups, A.group, x, ldx, codes, steps);
 }
@@ -240,7 +244,10 @@ int pack_t(const ActDims& A, const T* x, int64_t ldx, int8_t* codes, float* step
     // whole groups in each unit
     const Cover c = cover(A.rows, div_up(div_up(A.cols, 8), G) * G, kPackUnits);
     if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
-    auto* k = A.cols % 8 ? k_act_pack_lanes<T, true> : k_act_pack_lanes<T, false>;
+    const RowEnd end = row_end(A.cols);
+    auto* k = end == kWhole    ? k_act_pack_lanes<T, kWhole>
+              : end == kRagged ? k_act_pack_lanes<T, kRagged>
+                               : k_act_pack_lanes<T, kTiny>;
     k<<<c.blocks, kBlock, 0, st>>>(
         A.rows, (int)A.cols, (int)A.pitch, A.groups, log2_up(G), c.turns, c.tlog, x, ldx, codes,
         steps);
@@ -265,7 +272,7 @@ int unpack_t(const ActDims& A, const int8_t* codes, const float* steps, T* x,
   if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
   int glog = 31;  // one step per row: index 0
   if (!A.whole_row) glog = log2_up(A.group);
-  auto* k = A.cols % 8 ? k_act_unpack<T, true> : k_act_unpack<T, false>;
+  auto* k = A.cols % 8 ? k_act_unpack<T, kRagged> : k_act_unpack<T, kWhole>;
   k<<<c.blocks, kBlock, 0, st>>>(
       A.rows, (int)A.cols, (int)A.pitch, A.groups, glog, c.turns, c.tlog, codes, steps, x,
       ldx);

@@ -62,15 +62,22 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* red) {
   return m;
 }
 
-template <bool RAGGED>
-__device__ __forceinline__ void load_vec(const float* __restrict__ p, int c, int cols,
-                                         float none, float (&f)[8]) {
-  if (p == nullptr) {
+// A vector's columns, or `none` where there is no vector; settled later.
+template <int END>
+__device__ __forceinline__ Raw8<float> load_vec(const float* __restrict__ p, int c, int cols,
+                                                float none) {
+  if (p != nullptr) return load_chunk<END>(p, c, cols);
+  Raw8<float> r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = none;
-  } else {
-    widen(load_chunk<RAGGED>(p, c, cols), f);
-  }
+  for (int j = 0; j < 8; ++j) r.v[j] = none;
+  return r;
+}
+
+template <int END>
+__device__ __forceinline__ void use_vec(Raw8<float> r, const float* p, int c, int cols,
+                                        float (&f)[8]) {
+  if (p != nullptr) settle<END>(r, c, cols);
+  widen(r, f);
 }
 
 // The 8-bit form of a row held as f[R][8]: one step per 2^Glog lanes, or (Glog
@@ -109,9 +116,7 @@ __device__ __forceinline__ void pack_row(const float (&f)[R][8], int lane, int p
 // One row per NT threads; a workgroup of BT threads walks BT / NT rows at a
 // time.  2^Glog lanes share a step of the 8-bit forms written in the same pass
 // (Glog < 0: the row does).
-// RAGGED: the last chunk of a row may be short (cols % 8 != 0); otherwise a
-// chunk is a row's or past its end as a whole.
-template <typename T, int NT, int R, bool RAGGED>
+template <typename T, int NT, int R, int END>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
     int64_t rows, int cols, int pitch, int groups, int Glog, LayerNormArgs a) {
   constexpr int BT = NT < 256 ? 256 : NT;
@@ -124,18 +129,22 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
   const int64_t stride = (int64_t)gridDim.x * PER;
   int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / NT;
   if (row >= rows) return;  // whole waves; the whole workgroup where PER = 1
+  // everything is on its way before anything is used
+  Raw8<T> raw[R];
+  Raw8<float> rw[R], rb[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int c = (lane + i * NT) * 8;
+    raw[i] = load_chunk<END>(x + row * a.ldx, c, cols);
+    rw[i] = load_vec<END>(a.weight, c, cols, 1.f);
+    rb[i] = load_vec<END>(a.bias, c, cols, 0.f);
+  }
   float w[R][8], b[R][8];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int c = (lane + i * NT) * 8;
-    load_vec<RAGGED>(a.weight, c, cols, 1.f, w[i]);
-    load_vec<RAGGED>(a.bias, c, cols, 0.f, b[i]);
-  }
-  Raw8<T> raw[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int c = (lane + i * NT) * 8;
-    raw[i] = load_chunk<RAGGED>(x + row * a.ldx, c, cols);
+    use_vec<END>(rw[i], a.weight, c, cols, w[i]);
+    use_vec<END>(rb[i], a.bias, c, cols, b[i]);
   }
   const float n = (float)cols;
   int phase = 0;
@@ -143,6 +152,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
     float f[R][8], sum = 0.f, none = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
+      settle<END>(raw[i], (lane + i * NT) * 8, cols);
       widen(raw[i], f[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum += f[i][j];
@@ -152,7 +162,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
-        raw[i] = load_chunk<RAGGED>(x + next * a.ldx, c, cols);
+        raw[i] = load_chunk<END>(x + next * a.ldx, c, cols);
       }
     }
     if (a.x_codes)
@@ -169,7 +179,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         f[i][j] -= mean;
-        if (RAGGED && c + j >= cols) f[i][j] = 0.f;
+        if (END != kWhole && c + j >= cols) f[i][j] = 0.f;
         q = fmaf(f[i][j], f[i][j], q);
       }
       ss += c < cols ? q : 0.f;
@@ -187,13 +197,13 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_norm(
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
       const Raw8<T> o = narrow<T>(f[i]);
-      if (y) store_chunk<RAGGED>(y + row * a.ldy + c, o, cols - c);
+      if (y) store_chunk<END>(y + row * a.ldy + c, o, cols - c);
       if (a.y_codes) {
         // the form of y as it is stored; columns past the last are 0
         widen(o, f[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (RAGGED ? c + j >= cols : c >= cols) f[i][j] = 0.f;
+          if (END != kWhole ? c + j >= cols : c >= cols) f[i][j] = 0.f;
       }
     }
     if (a.y_codes)
@@ -235,8 +245,8 @@ __global__ __launch_bounds__(1024) void k_layer_norm_long(int64_t rows, int cols
     for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
       float w[8], b[8];
       widen(load8(x + c, cols - c), f);
-      load_vec<true>(a.weight, c, cols, 1.f, w);
-      load_vec<true>(a.bias, c, cols, 0.f, b);
+      use_vec<kRagged>(load_vec<kRagged>(a.weight, c, cols, 1.f), a.weight, c, cols, w);
+      use_vec<kRagged>(load_vec<kRagged>(a.bias, c, cols, 0.f), a.bias, c, cols, b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean) * rstd, w[j], b[j]);
       store8((T*)a.y + row * a.ldy + c, narrow<T>(f), cols - c);
@@ -252,18 +262,22 @@ struct XChunk;
 template <typename T>
 struct XChunk<T, false> {
   Raw8<T> raw;
-  template <bool RAGGED>
+  template <int END>
   __device__ __forceinline__ void load(const LayerNormBackArgs& a, int64_t row, int c,
                                        int cols, int, int, int) {
-    raw = load_chunk<RAGGED>((const T*)a.x + row * a.ldx, c, cols);
+    raw = load_chunk<END>((const T*)a.x + row * a.ldx, c, cols);
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const { widen(raw, f); }
+  template <int END>
+  __device__ __forceinline__ void get(float (&f)[8], int c, int cols) {
+    settle<END>(raw, c, cols);
+    widen(raw, f);
+  }
 };
 template <typename T>
 struct XChunk<T, true> {
   uint2 w;
   float step;
-  template <bool RAGGED>
+  template <int END>
   __device__ __forceinline__ void load(const LayerNormBackArgs& a, int64_t row, int c,
                                        int cols, int pitch, int groups, int glog) {
     w = make_uint2(0, 0);
@@ -273,13 +287,16 @@ struct XChunk<T, true> {
       step = a.steps[row * groups + (c >> glog)];
     }
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const { decode8(w, step, f); }
+  template <int END>
+  __device__ __forceinline__ void get(float (&f)[8], int, int) {
+    decode8(w, step, f);
+  }
 };
 
 // Streams of NT threads walk the rows; BT / NT streams share a workgroup and
 // add their gradients in LDS.  Partial sums of workgroup b:
 // ws[b][0][cols] (weight), ws[b][1][cols] (bias).  GRAD = false: dx only.
-template <typename T, int NT, int R, int BT, bool FORM, bool GRAD, bool RAGGED>
+template <typename T, int NT, int R, int BT, bool FORM, bool GRAD, int END>
 __global__ __launch_bounds__(BT) void k_layer_norm_backward(
     int64_t rows, int cols, int pitch, int groups, int glog, LayerNormBackArgs a) {
   constexpr int S = BT / NT;
@@ -291,9 +308,10 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
   const int64_t stride = (int64_t)gridDim.x * S;
   const int64_t first = (int64_t)blockIdx.x * S;
   float w[R][8], gw[R][8], gb[R][8];
+  Raw8<float> rw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    load_vec<RAGGED>(a.weight, (lane + i * NT) * 8, cols, 1.f, w[i]);
+    rw[i] = load_vec<END>(a.weight, (lane + i * NT) * 8, cols, 1.f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) gw[i][j] = gb[i][j] = 0.f;
   }
@@ -305,14 +323,17 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int c = (lane + i * NT) * 8;
-        rdy[i] = load_chunk<RAGGED>((const T*)a.dy + row * a.lddy, c, cols);
-        rx[i].template load<RAGGED>(a, row, c, cols, pitch, groups, glog);
+        rdy[i] = load_chunk<END>((const T*)a.dy + row * a.lddy, c, cols);
+        rx[i].template load<END>(a, row, c, cols, pitch, groups, glog);
       }
       mean = a.mean[row];
       rstd = a.rstd[row];
     }
   };
   fetch(first + stream);
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    use_vec<END>(rw[i], a.weight, (lane + i * NT) * 8, cols, w[i]);
   const float n = (float)cols;
   int phase = 0;
   for (int64_t base = first; base < rows; base += stride) {
@@ -323,8 +344,9 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (lane + i * NT) * 8;
+      settle<END>(rdy[i], c, cols);
       widen(rdy[i], d[i]);
-      rx[i].get(xh[i]);
+      rx[i].template get<END>(xh[i], c, cols);
       if (!live) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[i][j] = xh[i][j] = 0.f;
@@ -334,7 +356,7 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
         // past the end dy is 0 and (x - mu) is not: only dy counts there, but
         // a NaN or an infinity in mu or rs has to stay out
         xh[i][j] = (xh[i][j] - mu) * rs;
-        if (RAGGED ? c + j >= cols : c >= cols) xh[i][j] = 0.f;
+        if (END != kWhole ? c + j >= cols : c >= cols) xh[i][j] = 0.f;
         if constexpr (GRAD) {
           gw[i][j] = fmaf(d[i][j], xh[i][j], gw[i][j]);
           gb[i][j] += d[i][j];
@@ -354,7 +376,7 @@ __global__ __launch_bounds__(BT) void k_layer_norm_backward(
         const int c = (lane + i * NT) * 8;
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[i][j] = rs * (d[i][j] - fmaf(xh[i][j], m2, m1));
-        store_chunk<RAGGED>((T*)a.dx + row * a.lddx + c, narrow<T>(d[i]), cols - c);
+        store_chunk<END>((T*)a.dx + row * a.lddx + c, narrow<T>(d[i]), cols - c);
       }
     }
   }
@@ -405,9 +427,9 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
     XChunk<T, FORM> rx;
     for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
       widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
-      rx.template load<true>(a, row, c, cols, pitch, groups, glog);
-      rx.get(xh);
-      load_vec<true>(a.weight, c, cols, 1.f, w);
+      rx.template load<kRagged>(a, row, c, cols, pitch, groups, glog);
+      rx.template get<kRagged>(xh, c, cols);
+      use_vec<kRagged>(load_vec<kRagged>(a.weight, c, cols, 1.f), a.weight, c, cols, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float v = c + j < cols ? d[j] * w[j] : 0.f;
@@ -421,9 +443,9 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
     const float m1 = s1 / (float)cols, m2 = s2 / (float)cols;
     for (int c = (int)threadIdx.x * 8; c < cols; c += 8192) {
       widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
-      rx.template load<true>(a, row, c, cols, pitch, groups, glog);
-      rx.get(xh);
-      load_vec<true>(a.weight, c, cols, 1.f, w);
+      rx.template load<kRagged>(a, row, c, cols, pitch, groups, glog);
+      rx.template get<kRagged>(xh, c, cols);
+      use_vec<kRagged>(load_vec<kRagged>(a.weight, c, cols, 1.f), a.weight, c, cols, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         d[j] = rs * (d[j] * w[j] - fmaf((xh[j] - mu) * rs, m2, m1));
@@ -442,8 +464,8 @@ __global__ __launch_bounds__(256) void k_layer_norm_columns(
     const float mu = a.mean[row], rs = a.rstd[row];
     widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
     XChunk<T, FORM> rx;
-    rx.template load<true>(a, row, c, cols, pitch, groups, glog);
-    rx.get(xh);
+    rx.template load<kRagged>(a, row, c, cols, pitch, groups, glog);
+    rx.template get<kRagged>(xh, c, cols);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       gw[j] = fmaf(d[j], (xh[j] - mu) * rs, gw[j]);
@@ -527,7 +549,9 @@ struct Forward {
     constexpr int BT = NT < 256 ? 256 : NT, PER = BT / NT;
     const int64_t need = (A.rows + PER - 1) / PER, most = (int64_t)kCus * (2048 / BT);
     const unsigned g = (unsigned)(need < most ? need : most);
-    auto* k = A.cols % 8 ? k_layer_norm<T, NT, R, true> : k_layer_norm<T, NT, R, false>;
+    auto* k = A.cols % 8 ? k_layer_norm<T, NT, R, kRagged> : k_layer_norm<T, NT, R, kWhole>;
+    if constexpr (NT == 64 && R == 1)
+      if (row_end(A.cols) == kTiny) k = k_layer_norm<T, NT, R, kTiny>;
     k<<<g, BT, 0, st>>>(A.rows, (int)A.cols, (int)A.pitch, A.groups,
                         A.whole_row ? -1 : glog_of(A) - 3, a);
   }
@@ -556,8 +580,11 @@ struct Backward {
     constexpr int BT = kBackThreads<NT>, S = BT / NT;
     *parts = back_streams(A, NT, BT);
     const size_t lds = S > 1 && GRAD ? sizeof(float) * S * NT * R * 8 : 0;
-    auto* k = A.cols % 8 ? k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, true>
-                         : k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, false>;
+    auto* k = A.cols % 8 ? k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, kRagged>
+                         : k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, kWhole>;
+    if constexpr (NT == 64 && R == 1)
+      if (row_end(A.cols) == kTiny)
+        k = k_layer_norm_backward<T, NT, R, BT, FORM, GRAD, kTiny>;
     k<<<(unsigned)*parts, BT, lds, st>>>(A.rows, (int)A.cols, (int)A.pitch, A.groups,
                                          glog_of(A), a);
   }
