@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "act.hpp"
+#include "act_bounds.hpp"
 
 namespace gq {
 namespace {
@@ -33,6 +34,7 @@ struct WgradArgs {
   int out, cols, pitch, groups, glog;
   const void* dy;
   int64_t lddy;
+  int64_t free_rows;   // rows of dy that a chunk may run out of
   const int8_t* codes;
   const float* steps;
   float beta;
@@ -153,14 +155,15 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   // through registers: pieces of eight columns, BO / 8 per row
   constexpr int AP = COPY ? 1 : BK * BO / 8 / TH;
   Raw8<T> ra[AP];
-  // A short last chunk may run on into the next row, and columns past the
-  // last hold anything; only the steps that reach the last row take care to
-  // stay inside it.
+  // A short last chunk may run on into the rows that follow (up to seven values
+  // behind the row's last one: seven rows where a row is one value), and
+  // columns past the last hold anything; only the steps that reach a row
+  // without that much behind it take care to stay inside theirs.
   const int odd = min(tid % LPR * 8, a.out - 1 - o0);
   auto load_dy = [&](int st) {
     const int64_t first = t0 + (int64_t)st * BK + tid / LPR;
     const T* r = (const T*)dy + first * a.lddy;
-    if (t0 + (int64_t)(st + 1) * BK < a.rows) {
+    if (t0 + (int64_t)(st + 1) * BK <= a.free_rows) {
 #pragma unroll
       for (int i = 0; i < AP; ++i)
         __builtin_memcpy(&ra[i], r + i * (TH / LPR) * a.lddy + odd, sizeof(ra[i]));
@@ -502,8 +505,9 @@ int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy
   float* w = (float*)ws;
   const int64_t wn = p.splits > 1 ? p.splits * quads(out * A.cols) : 0;
   const WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, glog,
-                       dy,     lddy,     codes,       steps,        beta,     dw,
-                       db,     w,        w + wn,      p.splits,     p.otiles, p.ctiles,
+                       dy,     lddy,     rows_with_room(A.rows, lddy, 7),
+                       codes,  steps,    beta,        dw,           db,
+                       w,      w + wn,   p.splits,    p.otiles,     p.ctiles,
                        p.turns, p.per};
   // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
   const bool copy = A.dtype != GQ_F32 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
