@@ -211,17 +211,14 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], const Step& s) {
   return r;
 }
 
-// x^ of four codes: bytes biased to unsigned (by 127, so that the bias times
-// the largest step is finite; codes are -127 .. 127) convert in one
-// instruction each, and (byte - 127) * step is exact in the fused
-// multiply-add.
+// x^ of four codes, -128 .. 127: each byte converts with its sign in one
+// instruction, and the product with a power of two is exact (it overflows only
+// for -128 at the largest step, whose x^ no type holds).
 __device__ __forceinline__ void decode4(uint32_t w, float step, float* f) {
-  w = (w ^ 0x80808080u) - 0x01010101u;
-  const float off = -127.f * step;
-  f[0] = fmaf((float)(w & 255u), step, off);
-  f[1] = fmaf((float)((w >> 8) & 255u), step, off);
-  f[2] = fmaf((float)((w >> 16) & 255u), step, off);
-  f[3] = fmaf((float)(w >> 24), step, off);
+  f[0] = (float)(int8_t)w * step;
+  f[1] = (float)(int8_t)(w >> 8) * step;
+  f[2] = (float)(int8_t)(w >> 16) * step;
+  f[3] = (float)((int32_t)w >> 24) * step;
 }
 
 __device__ __forceinline__ void decode8(uint2 w, float step, float (&f)[8]) {

@@ -347,7 +347,9 @@ int gq_elias_decode(const gq_desc* desc, int64_t n, const uint64_t* offsets,
  * integer, ties to even.  An all-zero group has step 0.  A group that holds a
  * NaN or an infinity has step NaN and codes 0: it decodes as NaN, and its
  * neighbours are untouched.  With a power of two x^ is exact in bf16 and
- * fp32, so the operators below round nothing when they read it.
+ * fp32, so the operators below round nothing when they read it.  A form may
+ * also come from elsewhere: its codes may be any of -128 .. 127 (0 past the
+ * last column), where -128 at the largest step has no finite x^.
  *
  * Conventions of these calls, beyond those at the top: activations are device
  * pointers with a row stride ld (in elements, ld >= cols; columns are
