@@ -9,11 +9,12 @@
 // comes from HBM), unpack 30 us, 6.8 TB/s (its codes from the last-level
 // cache); 8192 x 4096 with a step per row: 24 us.
 #include "act.hpp"
+#include "act_bounds.hpp"
 
 namespace gq {
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = kCoverThreads;
 
 // A unit is what a workgroup takes at once: kBlock / tpr rows by tpr chunks
 // (tpr a power of two, `turns` units side by side cover the rows).  Each
@@ -190,32 +191,6 @@ __global__ __launch_bounds__(kBlock) void k_act_unpack(
   }
 }
 
-int log2_up(int v) {
-  int p = 0;
-  while ((1 << p) < v) ++p;
-  return p;
-}
-
-// A launch holds fewer than 2^32 threads.
-constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / kBlock - 1;
-
-// Rows and chunks of a unit-wise kernel: chunks per row -> threads per row,
-// units side by side, workgroups (0: too many for one launch).
-struct Cover {
-  int tlog, turns;
-  unsigned blocks;
-};
-
-Cover cover(int64_t rows, int chunks, int at_once) {
-  Cover c;
-  c.tlog = log2_up(chunks < kBlock ? chunks : kBlock);
-  c.turns = div_up(chunks, 1 << c.tlog);
-  const int64_t per = kBlock >> c.tlog, units = (rows + per - 1) / per * c.turns;
-  const int64_t blocks = (units + at_once - 1) / at_once;
-  c.blocks = blocks <= kMaxBlocks ? (unsigned)blocks : 0;
-  return c;
-}
-
 // Workgroups over `n` items of which each takes `per` at a time, the rest by
 // stride.
 unsigned blocks_for(int64_t n, int per, int most) {
@@ -240,17 +215,19 @@ template <typename T>
 int pack_t(const ActDims& A, const T* x, int64_t ldx, int8_t* codes, float* steps,
            hipStream_t st) {
   if (!A.whole_row && A.group <= 512) {
-    const int G = A.group / 8;
+    const int G = group_lanes(A.group, A.pitch);
     // whole groups in each unit
-    const Cover c = cover(A.rows, div_up(div_up(A.cols, 8), G) * G, kPackUnits);
-    if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
+    const Cover c(div_up(div_up(A.cols, 8), G) * G, kPackUnits);
     const RowEnd end = row_end(A.cols);
     auto* k = end == kWhole    ? k_act_pack_lanes<T, kWhole>
               : end == kRagged ? k_act_pack_lanes<T, kRagged>
                                : k_act_pack_lanes<T, kTiny>;
-    k<<<c.blocks, kBlock, 0, st>>>(
-        A.rows, (int)A.cols, (int)A.pitch, A.groups, log2_up(G), c.turns, c.tlog, x, ldx, codes,
-        steps);
+    for (int64_t r = 0; r < A.rows; r += c.rows) {
+      const int64_t n = A.rows - r < c.rows ? A.rows - r : c.rows;
+      k<<<(unsigned)c.blocks(n), kBlock, 0, st>>>(
+          n, (int)A.cols, (int)A.pitch, A.groups, log2_up(G), c.turns, c.tlog, x + r * ldx, ldx,
+          codes + r * A.pitch, steps + r * A.groups);
+    }
   } else {
     // pitch, not cols: padding codes are written by the group's threads too
     const int n8 = (int)(A.group < A.pitch ? A.group : A.pitch) / 8;
@@ -268,14 +245,16 @@ int pack_t(const ActDims& A, const T* x, int64_t ldx, int8_t* codes, float* step
 template <typename T>
 int unpack_t(const ActDims& A, const int8_t* codes, const float* steps, T* x,
              int64_t ldx, hipStream_t st) {
-  const Cover c = cover(A.rows, div_up(A.cols, 8), kUnpackUnits);
-  if (c.blocks == 0) return (int)hipErrorInvalidConfiguration;
+  const Cover c(div_up(A.cols, 8), kUnpackUnits);
   int glog = 31;  // one step per row: index 0
   if (!A.whole_row) glog = log2_up(A.group);
   auto* k = A.cols % 8 ? k_act_unpack<T, kRagged> : k_act_unpack<T, kWhole>;
-  k<<<c.blocks, kBlock, 0, st>>>(
-      A.rows, (int)A.cols, (int)A.pitch, A.groups, glog, c.turns, c.tlog, codes, steps, x,
-      ldx);
+  for (int64_t r = 0; r < A.rows; r += c.rows) {
+    const int64_t n = A.rows - r < c.rows ? A.rows - r : c.rows;
+    k<<<(unsigned)c.blocks(n), kBlock, 0, st>>>(
+        n, (int)A.cols, (int)A.pitch, A.groups, glog, c.turns, c.tlog, codes + r * A.pitch,
+        steps + r * A.groups, x + r * ldx, ldx);
+  }
   return (int)hipGetLastError();
 }
 

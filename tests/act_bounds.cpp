@@ -1,9 +1,13 @@
-// Walks the loads that k_act_wgrad makes of dy through registers
-// (csrc/act_wgrad.hip, load_dy) over small matrices and prints the first that
-// leaves its matrix.  The rule that picks the unchecked loads is the library's.
+// Walks index arithmetic of the 8-bit activation kernels on the host; prints
+// what is wrong.  The bounds and layouts are the library's (act_bounds.hpp).
+//   loads   the loads that k_act_wgrad makes of dy through registers
+//           (csrc/act_wgrad.hip, load_dy) stay inside their matrix
+//   cover   packing and unpacking (csrc/act_pack.hip) reach every chunk of every
+//           row once, in launches that the device takes
 #include <algorithm>
 #include <cstdio>
-#include <cstdlib>
+#include <cstring>
+#include <vector>
 
 #include "act_bounds.hpp"
 
@@ -34,7 +38,7 @@ static int64_t past_the_end(int64_t rows, int64_t out, int64_t ld, int bo, int b
   return worst;
 }
 
-int main() {
+static int loads() {
   int bad = 0;
   const int tiles[3][2] = {{256, 32}, {128, 64}, {128, 32}};
   for (auto& t : tiles)
@@ -60,6 +64,60 @@ int main() {
         std::printf("rows_with_room(100, %lld, %lld) = %lld\n", (long long)ld,
                     (long long)past, (long long)r);
     }
+  return bad;
+}
+
+// The launches of `rows` rows: how often each chunk is reached.
+static bool covers(int64_t rows, int64_t chunks, int at_once, int64_t most) {
+  const gq::Cover c(chunks, at_once, most);
+  const int tpr = 1 << c.tlog, per = gq::kCoverThreads >> c.tlog;
+  std::vector<int> seen(rows * chunks);
+  if (c.rows < 1) return false;
+  for (int64_t r = 0; r < rows; r += c.rows) {
+    const int64_t n = std::min(rows - r, c.rows), blocks = c.blocks(n);
+    if (blocks < 1 || blocks > most) return false;
+    for (int64_t b = 0; b < blocks; ++b)
+      for (int64_t u = b * at_once; u < (b + 1) * at_once; ++u)
+        for (int t = 0; t < gq::kCoverThreads; ++t) {
+          const int64_t row = u / c.turns * per + t / tpr, ch = u % c.turns * tpr + t % tpr;
+          if (row < n && ch < chunks) ++seen[(r + row) * chunks + ch];
+        }
+  }
+  return std::all_of(seen.begin(), seen.end(), [](int v) { return v == 1; });
+}
+
+static int cover() {
+  int bad = 0;
+  for (int64_t rows : {1, 3, 64, 65, 500})
+    for (int64_t chunks : {1, 2, 5, 64, 200, 256, 257, 600})
+      for (int at_once : {1, 2})
+        for (int64_t most : {3, 7, 1000})
+          if (!covers(rows, chunks, at_once, most) && bad++ < 5)
+            std::printf("cover: %lld rows of %lld chunks, %d units, %lld workgroups\n",
+                        (long long)rows, (long long)chunks, at_once, (long long)most);
+  // the largest matrices of every width and group: all taken, in 257 launches at
+  // most (2^38 rows of one column, 64 of them per workgroup)
+  for (int64_t cols = 1; cols <= 1 << 20; cols = cols < 300 ? cols + 1 : cols * 3 / 2)
+    for (int group = 32; group <= 1024; group *= 2) {
+      const int64_t rows = (int64_t(1) << 38) / cols, pitch = (cols + 15) / 16 * 16;
+      const int G = gq::group_lanes(group, pitch);
+      const int64_t whole = ((cols + 7) / 8 + G - 1) / G * G;
+      const bool pack = group <= 512;       // longer groups: a walk by stride
+      const gq::Cover c = pack ? gq::Cover(whole, 1) : gq::Cover((cols + 7) / 8, 2);
+      const int64_t first = std::min(rows, c.rows), n = (rows + c.rows - 1) / c.rows;
+      // a group lies in one row's lanes, and all of the pitch is written
+      const bool fits = !pack || (G >= 4 && G <= 64 && (G & (G - 1)) == 0 && G <= 1 << c.tlog &&
+                                  (G == group / 8 || G >= pitch / 8) && whole * 8 >= pitch);
+      if ((c.blocks(first) > gq::kCoverBlocks || !fits || n > 257) && bad++ < 5)
+        std::printf("cover: %lld x %lld, group %d: %lld launches of %lld workgroups\n",
+                    (long long)rows, (long long)cols, group, (long long)n,
+                    (long long)c.blocks(first));
+    }
+  return bad;
+}
+
+int main(int argc, char** argv) {
+  const int bad = argc > 1 && !std::strcmp(argv[1], "cover") ? cover() : loads();
   std::printf("%d bad\n", bad);
   return bad != 0;
 }

@@ -1,6 +1,7 @@
-"""Index bounds of the 8-bit activation kernels, on the CPU: the loads of the
-weight gradient's way through registers stay inside dy.  The bounds are plain
-C++ that the library shares (csrc/act_bounds.hpp)."""
+"""Index arithmetic of the 8-bit activation kernels, on the CPU: the loads of the
+weight gradient's way through registers stay inside dy, and packing and
+unpacking reach every value of the largest matrices in launches that the device
+takes.  The rules are plain C++ that the library shares (csrc/act_bounds.hpp)."""
 import os
 import shutil
 import subprocess
@@ -21,6 +22,7 @@ def walk(tmp_path_factory):
     return exe
 
 
-def test_loads_stay_inside(walk):
-    r = subprocess.run([walk], capture_output=True, text=True, timeout=120)
+@pytest.mark.parametrize("what", ["loads", "cover"])
+def test_walk(walk, what):
+    r = subprocess.run([walk, what], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
