@@ -39,6 +39,7 @@ SYMBOLS = ("gq_code_bits", "gq_payload_size", "gq_select_levels",
 
 GQ_F32, GQ_BF16, GQ_F16 = 0, 1, 2
 DTYPES = {torch.float32: GQ_F32, torch.bfloat16: GQ_BF16, torch.float16: GQ_F16}
+TORCH_DTYPES = {v: k for k, v in DTYPES.items()}
 
 
 class gq_desc(C.Structure):
@@ -53,8 +54,26 @@ class gq_desc(C.Structure):
 
 
 class gq_act(C.Structure):
+    """Also has torch_dtype, pitch (bytes of a row of codes) and groups (steps
+    of a row), of the fields as they are."""
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64),
                 ("dtype", C.c_int32), ("group", C.c_int32)]
+
+    def __getattr__(self, name):
+        # on the first use after a field was set; the calls read them often
+        if name not in ("torch_dtype", "pitch", "groups"):
+            raise AttributeError(name)
+        gq_act_size(self)           # raises for what the library refuses
+        self.__dict__.update(
+            torch_dtype=TORCH_DTYPES[self.dtype],
+            pitch=-(-self.cols // 16) * 16,
+            groups=-(-self.cols // self.group) if self.group else 1)
+        return self.__dict__[name]
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        for known in ("torch_dtype", "pitch", "groups"):
+            self.__dict__.pop(known, None)
 
     def __repr__(self) -> str:
         return (f"gq_act(rows={self.rows}, cols={self.cols}, "
@@ -498,18 +517,14 @@ def act(rows: int, cols: int, dtype: torch.dtype = torch.bfloat16,
     if dtype not in DTYPES:
         raise TypeError(f"act: no activations of type {dtype}")
     a = gq_act(rows, cols, DTYPES[dtype], group)
-    a.torch_dtype = dtype
     gq_act_size(a)                  # raises for what the library refuses
-    a.ref = C.byref(a)
-    a.pitch = -(-cols // 16) * 16
-    a.groups = -(-cols // group) if group else 1
     return a
 
 
 def gq_act_size(a: gq_act):
     """(bytes of codes, number of steps) of the 8-bit form."""
     cb, ns = C.c_int64(), C.c_int64()
-    _check(_lib.gq_act_size(C.byref(a), C.byref(cb), C.byref(ns)),
+    _check(_lib.gq_act_size(a, C.byref(cb), C.byref(ns)),
            "gq_act_size")
     return cb.value, ns.value
 
@@ -601,7 +616,7 @@ def gq_act_pack(a: gq_act, x: torch.Tensor, codes: torch.Tensor,
                 steps: torch.Tensor, stream=None) -> None:
     px, ld = _matrix(x, a, a.cols, "x")
     pc, ps = _form(codes, steps, a, a.rows, "x")
-    _check(_lib.gq_act_pack(a.ref, px, ld, pc, ps, _queue(stream, x)),
+    _check(_lib.gq_act_pack(a, px, ld, pc, ps, _queue(stream, x)),
            "gq_act_pack")
 
 
@@ -609,13 +624,13 @@ def gq_act_unpack(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
                   x: torch.Tensor, stream=None) -> None:
     px, ld = _matrix(x, a, a.cols, "x")
     pc, ps = _form(codes, steps, a, a.rows, "x")
-    _check(_lib.gq_act_unpack(a.ref, pc, ps, px, ld, _queue(stream, x)),
+    _check(_lib.gq_act_unpack(a, pc, ps, px, ld, _queue(stream, x)),
            "gq_act_unpack")
 
 
 def gq_act_linear_workspace(a: gq_act, out: int) -> int:
     b = C.c_int64()
-    _check(_lib.gq_act_linear_workspace(a.ref, out, C.byref(b)),
+    _check(_lib.gq_act_linear_workspace(a, out, C.byref(b)),
            "gq_act_linear_workspace")
     return b.value
 
@@ -633,14 +648,14 @@ def gq_act_linear(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
     pc, ps = _form(codes, steps, a, a.rows, "x")
     wc, ws = _form(w_codes, w_steps, a, out, "weight")
     pw, nw = _space(workspace)
-    _check(_lib.gq_act_linear(a.ref, out, pc, ps, wc, ws,
+    _check(_lib.gq_act_linear(a, out, pc, ps, wc, ws,
                               _vec(bias, out, "bias"), py, ld, pw, nw,
                               _queue(stream, y)), "gq_act_linear")
 
 
 def gq_act_wgrad_workspace(a: gq_act, out: int) -> int:
     b = C.c_int64()
-    _check(_lib.gq_act_wgrad_workspace(a.ref, out, C.byref(b)),
+    _check(_lib.gq_act_wgrad_workspace(a, out, C.byref(b)),
            "gq_act_wgrad_workspace")
     return b.value
 
@@ -657,7 +672,7 @@ def gq_act_wgrad(a: gq_act, dy: torch.Tensor, codes: torch.Tensor,
     pd, ld = _matrix(dy, a, out, "dy")
     pc, ps = _form(codes, steps, a, a.rows, "x")
     pw, nw = _space(workspace)
-    _check(_lib.gq_act_wgrad(a.ref, out, pd, ld, pc, ps, beta,
+    _check(_lib.gq_act_wgrad(a, out, pd, ld, pc, ps, beta,
                              _buffer(dweight, torch.float32, out * a.cols,
                                      "dweight"),
                              _vec(dbias, out, "dbias"), pw, nw,
@@ -676,7 +691,7 @@ def gq_layer_norm(a: gq_act, x: torch.Tensor, weight: torch.Tensor | None,
     xc, xs = (None, None) if x_form is None else _form(*x_form, a, a.rows, "x")
     yc, ys = (None, None) if y_form is None else _form(*y_form, a, a.rows, "y")
     _check(_lib.gq_layer_norm(
-        a.ref, px, ldx, _vec(weight, a.cols, "weight"),
+        a, px, ldx, _vec(weight, a.cols, "weight"),
         _vec(bias, a.cols, "bias"), eps, py, ldy, _vec(mean, a.rows, "mean"),
         _vec(rstd, a.rows, "rstd"), xc, xs, yc, ys, _queue(stream, x)),
         "gq_layer_norm")
@@ -684,7 +699,7 @@ def gq_layer_norm(a: gq_act, x: torch.Tensor, weight: torch.Tensor | None,
 
 def gq_layer_norm_workspace(a: gq_act) -> int:
     b = C.c_int64()
-    _check(_lib.gq_layer_norm_workspace(a.ref, C.byref(b)),
+    _check(_lib.gq_layer_norm_workspace(a, C.byref(b)),
            "gq_layer_norm_workspace")
     return b.value
 
@@ -708,7 +723,7 @@ def gq_layer_norm_backward(a: gq_act, dy: torch.Tensor, x,
         pc, ps = _form(*x, a, a.rows, "x")
     pw, nw = _space(workspace)
     _check(_lib.gq_layer_norm_backward(
-        a.ref, pd, ldd, px, ldx or 0, pc, ps,
+        a, pd, ldd, px, ldx or 0, pc, ps,
         _vec(mean, a.rows, "mean"), _vec(rstd, a.rows, "rstd"),
         _vec(weight, a.cols, "weight"), po, ldo, beta,
         _vec(dweight, a.cols, "dweight"), _vec(dbias, a.cols, "dbias"),
