@@ -285,8 +285,10 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   int turn = 0;  // st % turns
   // Step st from (now_a, now_b), with step st + 1 prepared in (next_a, next_b)
   // and the codes of step st + 2 loaded.  All four are restrict: reads and
-  // writes here do not wait for the copies on their way to next_a.  Past the
-  // last step zeros are prepared.
+  // writes here do not wait for the copies on their way to next_a.  The barrier
+  // does: the compiler counts the copies as writes to LDS and waits before it
+  // for all but the loads of codes, which are younger (a test follows this in
+  // the assembly).  Past the last step zeros are prepared.
   auto step = [&](int st, LdsPtr __restrict__ now_a, LdsPtr __restrict__ now_b,
                   LdsPtr __restrict__ next_a, LdsPtr __restrict__ next_b) {
     turn = turn + 1 == a.turns ? 0 : turn + 1;
