@@ -469,27 +469,38 @@ __global__ __launch_bounds__(1024) void k_layer_norm_backward_long(
   }
 }
 
+// A workgroup takes every gridDim.y-th row.  64 of them at a time are added up
+// by themselves, so that a sum's longest chain of additions is 64 and one more
+// per 4096 rows, as in the shorter rows' pass.
 template <typename T, bool FORM>
 __global__ __launch_bounds__(256) void k_layer_norm_columns(
     int64_t rows, int cols, int pitch, int groups, int glog, LayerNormBackArgs a) {
   const int c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8;
   if (c >= cols) return;
-  float gw[8] = {}, gb[8] = {}, d[8], xh[8];
-  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-    const float mu = a.mean[row], rs = a.rstd[row];
-    widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
-    XChunk<T, FORM> rx;
-    rx.template load<kRagged>(a, row, c, cols, pitch, groups, glog);
-    rx.template get<kRagged>(xh, c, cols);
+  float tw[8] = {}, tb[8] = {};
+  for (int64_t row = blockIdx.y; row < rows;) {
+    float gw[8] = {}, gb[8] = {}, d[8], xh[8];
+    for (int n = 0; n < 64 && row < rows; ++n, row += gridDim.y) {
+      const float mu = a.mean[row], rs = a.rstd[row];
+      widen(load8((const T*)a.dy + row * a.lddy + c, cols - c), d);
+      XChunk<T, FORM> rx;
+      rx.template load<kRagged>(a, row, c, cols, pitch, groups, glog);
+      rx.template get<kRagged>(xh, c, cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        gw[j] = fmaf(d[j], (xh[j] - mu) * rs, gw[j]);
+        gb[j] += d[j];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      gw[j] = fmaf(d[j], (xh[j] - mu) * rs, gw[j]);
-      gb[j] += d[j];
+      tw[j] += gw[j];
+      tb[j] += gb[j];
     }
   }
   float* o = a.ws + (int64_t)blockIdx.y * 2 * cols;
-  store8(o + c, narrow<float>(gw), cols - c);
-  store8(o + cols + c, narrow<float>(gb), cols - c);
+  store8(o + c, narrow<float>(tw), cols - c);
+  store8(o + cols + c, narrow<float>(tb), cols - c);
 }
 
 // dweight / dbias <- beta * old + the parts' sum.  32 columns by 32 slices of
