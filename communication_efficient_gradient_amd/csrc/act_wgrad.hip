@@ -12,7 +12,8 @@
 //   fp16  x^ is exact in fp16: steps are at most 2^9, and one below 2^-24 comes
 //         with values that are multiples of 2^-24 and kept as they are
 //   fp32  dy is split into three bf16 terms (24 significant bits) whose sum is
-//         the value itself, one matrix product each with x^ in bf16
+//         the value itself, one matrix product each with x^ in bf16; below
+//         2^-110 the third term is cut at bf16's last place, 2^-133
 #include <type_traits>
 
 #include "act.hpp"

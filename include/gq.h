@@ -404,9 +404,10 @@ int gq_act_linear(const gq_act* act, int64_t out, const int8_t* codes,
 /* Gradients of a linear layer whose input is kept in 8 bits:
  *   dweight[o, c] <- beta * dweight[o, c] + sum_t dy[t, o] * x^[t, c]
  *   dbias[o]      <- beta * dbias[o]      + sum_t dy[t, o]
- * dy [rows, out] in act's type, used in full (fp32 is not rounded to bf16);
- * products are exact for forms that gq_act_pack writes from that type, the
- * sums are fp32.  dweight fp32 [out][cols], contiguous: a slice of the flat
+ * dy [rows, out] in act's type, used in full (fp32 is not rounded to bf16, but
+ * kept to multiples of 2^-133, which is exact from 2^-110 on, and an infinity in
+ * it gives NaN); products are exact for forms that gq_act_pack writes from that
+ * type, the sums are fp32.  dweight fp32 [out][cols], contiguous: a slice of the flat
  * gradient that gq_quantize takes.  dbias may be NULL. */
 int gq_act_wgrad_workspace(const gq_act* act, int64_t out, int64_t* bytes);
 int gq_act_wgrad(const gq_act* act, int64_t out, const void* dy, int64_t lddy,
