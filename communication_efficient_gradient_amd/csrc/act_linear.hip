@@ -293,8 +293,8 @@ __global__ __launch_bounds__(256) void k_act_linear_join(LinearArgs a) {
 
 // Few tokens.  A workgroup takes 16 * MT tokens by 16 * NT outputs; its eight
 // waves take turns of U * 64 codes along the sum and add up in LDS.  Operands
-// come straight from memory (the weight, once where MT covers the tokens) and
-// L2 in the products' layout, 16 codes of one row per lane, 16 rows by 64 codes
+// come straight from memory (the weight once up to 32 tokens, which MT covers,
+// twice above) and L2 in the products' layout, 16 codes of one row per lane, 16 rows by 64 codes
 // per instruction: nothing waits for a barrier until the sums are joined, and
 // U steps of loads per wave are in flight at once.
 constexpr int kFewWaves = 8;
@@ -389,9 +389,22 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_act_linear_few(LinearArgs a)
   }
 }
 
-// From 65 tokens on the tiled kernel is faster (64 x 4096 x 4096, tokens x out
-// x cols: 11 us here, 15 there; 203 x 2050 x 4100: 20 and 15).
-bool few_tokens(const ActDims& A) { return A.rows <= 64; }
+// Which of the two: each workgroup above reads the codes of all its tokens (up
+// to 32) from L2 for 16 or 32 outputs, the tiled kernel once for 64.  That is
+// little beside the weight up to 4 tokens; from there on what one CU reads so
+// decides.  Measured (us here / there, bf16, tokens x out x cols; the product
+// compared below behind it):
+//   16 x 8192 x 8192 17.5 / 21.5 (32)    17 x 8192 x 8192  18.9 / 21.7 (34)
+//   64 x 4096 x 4096 10.3 / 12.7 (32)     8 x 20000 x 8192 40.1 / 36.3 (40)
+//   16 x 9216 x 8192 24.2 / 21.8 (48)    12 x 16384 x 8192 30.1 / 23.2 (48)
+//   32 x 4608 x 8192 23.8 / 21.5 (64)    64 x 16384 x 8192 79.8 / 25.7 (128)
+//    4 x 50000 x 4096 42.8 / 47.4         1 x 16384 x 8192 24.1 / 22.8
+// Past 64 tokens the tiled kernel: 65 x 4096 x 4096 15.0 / 12.8.
+bool few_tokens(const ActDims& A, int64_t out) {
+  if (A.rows <= 4 || A.rows > 64) return A.rows <= 4;
+  const int groups = A.rows <= 32 ? div_up(out, 16) : 2 * div_up(out, 32);
+  return div_up(groups, kCus) * (A.rows < 32 ? A.rows : 32) < 48;
+}
 
 template <typename T, int MT, int NT, int U>
 void few(const LinearArgs& a, hipStream_t st) {
@@ -415,11 +428,12 @@ struct Plan {
 Plan plan_linear(const ActDims& A, int64_t out) {
   const int kt = div_up(A.pitch, 128);
   Plan best = {1, kt, 0};
-  if (few_tokens(A)) return best;
+  if (few_tokens(A, out)) return best;
   double least = 1e30;
   for (int tile = 64; tile <= 256; tile *= 2) {
     const int64_t tiles = ((A.rows + tile - 1) / tile) * ((out + tile - 1) / tile);
-    for (int s = 1; s <= 8 && (s == 1 || kt / s >= 8); ++s) {
+    // up to 64 tokens unsplit: their products need no workspace
+    for (int s = 1; s <= 8 && (s == 1 || (A.rows > 64 && kt / s >= 8)); ++s) {
       const int per = div_up(kt, s);
       const int64_t groups = tiles * s;
       const double rounds = (double)((groups + kCus - 1) / kCus);
@@ -440,7 +454,7 @@ Plan plan_linear(const ActDims& A, int64_t out) {
 
 template <typename T>
 int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
-  if (few_tokens(A)) {
+  if (few_tokens(A, a.out)) {
     if (A.rows <= 16) few<T, 1, 1, 8>(a, st);
     else if (A.rows <= 32) few<T, 2, 1, 4>(a, st);
     else few<T, 2, 2, 4>(a, st);

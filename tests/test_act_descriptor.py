@@ -66,3 +66,10 @@ def test_calls_check_the_type_of_a_direct_descriptor(gq):
     host = torch.zeros(4, 6, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="device tensor"):
         gq.gq_act_pack(a, host, torch.zeros(4, 16, dtype=torch.int8), torch.zeros(4, 1))
+
+
+@pytest.mark.parametrize("rows", [1, 8, 9, 16, 17, 33, 64])
+def test_few_tokens_need_no_workspace(gq, rows):
+    for out in (1, 64, 4097, 8193, 40000, 1 << 18):
+        for cols in (1, 1000, 16384, 131071):
+            assert gq.gq_act_linear_workspace(gq.act(rows, cols, torch.bfloat16), out) == 0
