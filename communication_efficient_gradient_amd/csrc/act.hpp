@@ -90,8 +90,8 @@ __device__ __forceinline__ void shift_down(Raw8<T>& r, int n) {
 // settle() moves it down where it is used.  kTiny: fewer than eight columns,
 // read by elements.  A way through elements, or moving the values where they
 // are loaded, makes loads of the wave wait for those before (backward pass of
-// 1531 x 1001 fp16: 8.9 us with both in the kernel, 7.9 so; layer norm of 16384
-// x 4096 bf16 with its input's 8-bit form: 93 us through elements, 68 with whole
+// 1531 x 1001 fp16: 8.9 us with both in the kernel, 7.8 so; layer norm of 16384
+// x 4096 bf16 with its input's 8-bit form: 93 us through elements, 62 with whole
 // chunks).
 enum RowEnd { kWhole = 0, kRagged = 1, kTiny = 2 };
 
@@ -239,8 +239,9 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t m, int G) {
 
 // ------------------------------------------------- global memory to LDS --
 // A range of global memory that reads as zeros past its end (ranges of 4 GiB
-// and more are cut there; a length below zero is none).  The accesses below are buffer instructions: the
-// bounds are checked by the load itself, and unlike the global form they do
+// and more are cut there; a length below zero is none).  The accesses below are
+// buffer instructions: the bounds are checked by the load itself, on the sum of
+// its offsets, the scalar one included, and unlike the global form they do
 // not make the compiler drain all LDS reads in flight before it uses one.
 typedef __amdgpu_buffer_rsrc_t BufferRange;
 

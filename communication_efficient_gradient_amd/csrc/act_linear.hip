@@ -6,9 +6,9 @@
 // Both operands are rows of int8 along the summed axis, 16-byte aligned and
 // zero-padded, which is the layout the matrix instructions take: 16 (32x32x32)
 // consecutive codes per lane, straight from LDS.  8192 x 8192 x 4096 (tokens x
-// out x cols): 254 to 262 us, 2.1 POP/s (2.66 within the k-tiles); one token
-// through 4096 x 4096: 5.3 us, 3.2 TB/s of weight, and through 16384 x 8192 25
-// us, 5.3 TB/s.
+// out x cols): 233 us in a loop, 2.4 POP/s, median 272 (255 to 293) under the
+// profiler; one token through 4096 x 4096: median 6.3 us (5.2 to 6.6), 2.7 TB/s
+// of weight, and through 16384 x 8192 24 us, 5.6 TB/s.
 #include "act.hpp"
 
 namespace gq {
@@ -420,11 +420,11 @@ struct Plan {
 // The tile's side and the number of splits by an estimate of the time in
 // microseconds: rounds of tiles over the chip, their k-tiles, what a tile costs
 // besides, and the splits' sums through memory.  Measured (tokens x out x
-// cols): 4096 x 4096 x 4096 63 us with 256-tiles, 75 with 128; 1024 x 4096 x
-// 4096 25 us with 128-tiles, 36 with 64, 43 with 256; 512 x 4096 x 4096 18 us
-// with 64, 20 with 128; two splits only pay for long sums on few tiles (8192 x
-// 512 x 8192: 50 us unsplit, 68 with two, both with the 128-tiles of two
-// k-tiles in LDS that take 42 now with four).
+// cols): 4096 x 4096 x 4096 62 us with 256-tiles, 82 with 128; 1024 x 4096 x
+// 4096 25 us with 128-tiles, 34 with 64, 43 with 256; 512 x 4096 x 4096 17.1 us
+// with 64, 18.8 with 128; splits only pay for long sums on few tiles (8192 x 512
+// x 8192: 42 us unsplit, 73 with two; 512 x 512 x 32768: 73 unsplit, 44 with two,
+// 25 with as many as are taken).
 Plan plan_linear(const ActDims& A, int64_t out) {
   const int kt = div_up(A.pitch, 128);
   Plan best = {1, kt, 0};

@@ -5,9 +5,11 @@
 // columns (16 bytes of bf16), so a wave's access is contiguous; a group of up
 // to 512 columns lies in 4..64 neighbouring lanes and needs only lane
 // exchanges, a longer one goes through LDS.  16384 x 4096 bf16 with a step per
-// 128 columns: pack 44.5 us, 4.6 TB/s (a large copy's rate is 5.1; its input
+// 128 columns: pack 44 us, 4.6 TB/s (a large copy's rate is 5.1; its input
 // comes from HBM), unpack 30 us, 6.8 TB/s (its codes from the last-level
-// cache); 8192 x 4096 with a step per row: 24 us.
+// cache; 38 without); 8192 x 4096 with a step per row: 24 us.  Groups over
+// 16384 columns are read twice: 1024 x 40000 with a step per row 36 us, 24 with
+// one per 128 columns.
 #include "act.hpp"
 #include "act_bounds.hpp"
 

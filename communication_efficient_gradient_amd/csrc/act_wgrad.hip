@@ -106,9 +106,9 @@ __device__ __forceinline__ u32x4 packed(const float (&f)[8]) {
 // rows; otherwise through registers, split into the type's bf16 terms) and
 // its codes, loaded one step earlier, are decoded into LDS.  A step of 256 x
 // 256 moves 260 KB through LDS and keeps the matrix cores busy for 2048 cycles:
-// the two share the time.  16384 x 4096 x 4096 (tokens x out x cols): 480 to
-// 505 us in bf16 and fp16, 1.1 PFLOP/s, matrix cores 58 % busy at 1.9 GHz;
-// fp32 340 us for 4096 x 4096 x 4096.
+// the two share the time.  16384 x 4096 x 4096 (tokens x out x cols): 455 us in
+// a loop in bf16 and 468 in fp16, 1.2 PFLOP/s, median 525 (504 to 625) under the
+// profiler, matrix cores 60 % busy; fp32 326 us for 4096 x 4096 x 4096.
 template <typename T, bool COPY, int BO, int BC, int WO, int WC, int BK>
 __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(WgradArgs a) {
   constexpr int P = kPlanes<T>;
@@ -448,10 +448,10 @@ struct Plan {
 // microseconds: rounds of workgroups (one 256 x 256 tile or two 128 x 128
 // tiles per CU), a step of 64 tokens each, what a tile costs besides, and the
 // parts' way through memory and back.  Measured (bf16, whole call): 16384 x
-// 2048 x 2048 tokens x out x cols 158 us with 256-tiles and 4 splits, 200 with
-// 128-tiles and 2; 8192 x 1024 x 1024 47 us with 256 and 16, 43.5 with 128 and
-// 8; 512 x 1024 x 4096 28 and 19 us unsplit; 8192 x 256 x 256 28.5 and 18 us
-// with 16 splits.
+// 2048 x 2048 tokens x out x cols 140 us with 256-tiles and 4 splits, 170 with
+// 128-tiles and 2; 8192 x 1024 x 1024 41.4 us with 256 and 13, 38.1 with 128 and
+// 8; 512 x 1024 x 4096 22.6 and 12.6 us unsplit; 8192 x 256 x 256 25.3 and 17.5 us
+// with 32 splits.
 Plan plan_wgrad(const ActDims& A, int64_t out) {
   const int64_t steps = (A.rows + 63) / 64;
   const double big_step = A.dtype == GQ_F32 ? 5.0 : 1.9;
@@ -475,8 +475,10 @@ Plan plan_wgrad(const ActDims& A, int64_t out) {
       }
     }
   }
-  // Shared out, the bias's sums need a second launch to join them (5 us); of
-  // up to 32 steps one tile takes all (0.15 us each).
+  // Shared out, the bias's sums need a second launch to join them (4 to 5 us);
+  // of up to 32 steps one tile takes all.  bf16: 1024 x 2048 x 2048 18.2 us so,
+  // 21.9 shared out, 2048 x 4096 x 2048 45.0 and 49.9, 4096 x 4096 x 4096 127 and
+  // 128, 16384 x 4096 x 4096 475 and 457.
   if (best.splits == 1 && steps <= 32) best.turns = 1;
   return best;
 }
@@ -517,7 +519,7 @@ int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy
                     lddy < (1 << 23) &&
                     out % 8 == 0;
   // Through registers 64-token steps of 256-tiles spill (16384 x 4095 x 4096
-  // bf16: 938 us, 693 with 32); fp32's three terms fill LDS with 32.
+  // bf16: 973 us, 547 with 32); fp32's three terms fill LDS with 32.
   if (A.dtype == GQ_F32) wgrad_t<float, false, 32, 32>(a, p.tile, st);
   else if (A.dtype == GQ_F16 && copy) wgrad_t<_Float16, true, 64, 64>(a, p.tile, st);
   else if (A.dtype == GQ_F16) wgrad_t<_Float16, false, 32, 64>(a, p.tile, st);

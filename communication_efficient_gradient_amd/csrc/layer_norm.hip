@@ -7,8 +7,8 @@
 //             dx = r (a - mean(a) - xh mean(a xh)),
 //             dw = sum_rows dy xh, db = sum_rows dy
 //
-// All of it is bound by HBM: a row is read once and stays in registers (R
-// chunks of eight columns in each of NT threads), so the forward pass moves
+// Up to 8192 columns all of it is bound by HBM: a row is read once and stays in
+// registers (R chunks of eight columns in each of NT threads), so the forward moves
 // 2 e bytes per value and the backward 3 e, or 2 e + 1 when it reads the
 // 8-bit form of x.  Statistics and gradients are fp32; the variance is taken
 // from the centred values in registers, which loses nothing where |mu| is
@@ -17,8 +17,16 @@
 // reduced, and each thread keeps the weight's and bias's gradient of its own
 // columns in registers.  A second launch adds the workgroups' partial sums
 // in a fixed order, so results repeat bit for bit.  16384 x 4096 bf16: forward
-// with its input's 8-bit form 60 to 67 us, 5.3 TB/s, backward from that form 70
-// us and 6.5 for the partial sums (a large copy's rate is 5.1 TB/s).
+// with its input's 8-bit form 62 us, 5.4 TB/s, backward from that form 70 us and
+// 6.2 for the partial sums (a large copy's rate is 5.1 TB/s); forward with its
+// output's form 67 us, 92 as norm and pack.
+//
+// Two widths are further from that.  From 8193 to 16384 columns the backward
+// pass with gradients has no registers for all it keeps (128 per thread: 108 to
+// 220 bytes of scratch a lane): 4096 x 12288 bf16 182 us from x and 216 from the
+// 8-bit form, 51 without gradients.  Over 16384 columns rows are read again:
+// three times forward (4096 x 20000 bf16 176 us), twice backward and once more
+// for the column sums (280 us).
 #include "act.hpp"
 
 namespace gq {
