@@ -360,29 +360,29 @@ def _own(s):
 
         if op == "weight":
             k["act"] = gq.act(o, c, t, BLOCK)
-            k["form"] = gq.alloc_fp8_weight(k["act"], e)
-            k["t_form"] = gq.alloc_fp8_weight(k["act"], e, transposed=True)
+            k["form"] = gq.alloc_block_weight(k["act"], e)
+            k["t_form"] = gq.alloc_block_weight(k["act"], e, transposed=True)
         else:
             r = case["rows"]
             k["act"] = gq.act(r, c, t, BLOCK)
             k["offsets"] = s["offsets"] if e > 1 else None
         if op == "linear":
-            k["form"], k["y"] = gq.alloc_fp8(k["act"]), new(r, o, dtype=t)
-            k["ws"] = gq.alloc_workspace(gq.gq_fp8_linear_workspace(k["act"], o, e))
+            k["form"], k["y"] = gq.alloc_block(k["act"]), new(r, o, dtype=t)
+            k["ws"] = gq.alloc_workspace(gq.gq_block_linear_workspace(k["act"], o, e))
         if op == "wgrad":
             k["dw"], k["db"] = new(e, o, c), new(e, o)
-            k["ws"] = gq.alloc_workspace(gq.gq_fp8_wgrad_workspace(k["act"], o, e))
+            k["ws"] = gq.alloc_workspace(gq.gq_block_wgrad_workspace(k["act"], o, e))
     a = k["act"]
     if op == "weight":
-        gq.gq_fp8_pack_weight(a, s["w"], k["form"], k["t_form"])
+        gq.gq_block_pack_weight(a, s["w"], k["form"], k["t_form"])
         return {"codes": k["form"][0], "steps": k["form"][1],
                 "t_codes": k["t_form"][0], "t_steps": k["t_form"][1]}
     if op == "linear":
-        gq.gq_fp8_pack(a, s["x"], *k["form"])
-        gq.gq_fp8_linear(a, *k["form"], s["w_codes"], s["w_steps"], s["bias"], k["y"],
+        gq.gq_block_pack(a, s["x"], *k["form"])
+        gq.gq_block_linear(a, *k["form"], s["w_codes"], s["w_steps"], s["bias"], k["y"],
                          offsets=k["offsets"], workspace=k["ws"])
         return {"y": k["y"]}
-    gq.gq_fp8_wgrad(a, s["dy"], s["codes"], s["steps"], k["dw"], k["db"],
+    gq.gq_block_wgrad(a, s["dy"], s["codes"], s["steps"], k["dw"], k["db"],
                     offsets=k["offsets"], workspace=k["ws"])
     return {"dweight": k["dw"], "dbias": k["db"]}
 
