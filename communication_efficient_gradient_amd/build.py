@@ -23,7 +23,8 @@ SOURCES = ["api.hip", "stream_quant.hip", "sort_quant.hip", "deq.hip",
            "layer_quant.hip", "topk_quant.hip", "elias.hip",
            "alloc_quant.hip", "binopt_quant.hip", "act_api.hip",
            "act_pack.hip", "layer_norm.hip", "act_linear.hip",
-           "act_wgrad.hip"]
+           "act_wgrad.hip", "step_api.hip", "fp8_pack.hip", "fp8_linear.hip",
+           "fp8_wgrad.hip", "adamw.hip"]
 ARCH = os.environ.get("GQ_OFFLOAD_ARCH", "gfx950")
 
 # -ffp-contract=off: the rounding decisions must see exactly the fp32

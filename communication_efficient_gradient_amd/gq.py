@@ -35,6 +35,10 @@ SYMBOLS = ("gq_code_bits", "gq_payload_size", "gq_select_levels",
            "gq_act_linear_workspace", "gq_act_linear",
            "gq_act_wgrad_workspace", "gq_act_wgrad", "gq_layer_norm",
            "gq_layer_norm_workspace", "gq_layer_norm_backward",
+           "gq_block_pack", "gq_block_unpack", "gq_block_pack_weight",
+           "gq_block_linear_workspace", "gq_block_linear",
+           "gq_block_wgrad_workspace", "gq_block_wgrad", "gq_adamw",
+           "gq_grad_norm_workspace", "gq_grad_norm",
            "gq_strerror", "gq_version")
 
 GQ_F32, GQ_BF16, GQ_F16 = 0, 1, 2
@@ -78,6 +82,16 @@ class gq_act(C.Structure):
     def __repr__(self) -> str:
         return (f"gq_act(rows={self.rows}, cols={self.cols}, "
                 f"dtype={self.dtype}, group={self.group})")
+
+
+class gq_adamw_desc(C.Structure):
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
+                ("eps", C.c_double), ("weight_decay", C.c_double),
+                ("bits", C.c_int32)]
+
+    def __repr__(self) -> str:
+        return (f"gq_adamw_desc(lr={self.lr}, beta1={self.beta1}, beta2={self.beta2}, "
+                f"eps={self.eps}, weight_decay={self.weight_decay}, bits={self.bits})")
 
 
 class GQError(RuntimeError):
@@ -134,6 +148,17 @@ def _load():
     lib.gq_layer_norm_workspace.argtypes = [A, C.POINTER(i64)]
     lib.gq_layer_norm_backward.argtypes = [A, P, i64, P, i64, P, P, P, P, P, P,
                                            i64, f32, P, P, P, i64, P]
+    lib.gq_block_pack.argtypes = [A, P, i64, P, P, P]
+    lib.gq_block_unpack.argtypes = [A, P, P, P, i64, P]
+    lib.gq_block_pack_weight.argtypes = [A, i32, P, P, P, P, P, P]
+    lib.gq_block_linear_workspace.argtypes = [A, i64, i32, C.POINTER(i64)]
+    lib.gq_block_linear.argtypes = [A, i64, i32, P, P, P, P, P, P, P, i64, P, i64, P]
+    lib.gq_block_wgrad_workspace.argtypes = [A, i64, i32, C.POINTER(i64)]
+    lib.gq_block_wgrad.argtypes = [A, i64, i32, P, P, i64, P, P, f32, P, P, P, i64, P]
+    lib.gq_adamw.argtypes = [C.POINTER(gq_adamw_desc), i64, i32, P, P, P, P, P, i64,
+                             P, P, P, P, P, P, P, i32, C.c_uint64, P]
+    lib.gq_grad_norm_workspace.argtypes = [i64, C.POINTER(i64)]
+    lib.gq_grad_norm.argtypes = [i64, P, f32, P, P, P, i64, P]
     lib.gq_strerror.argtypes = [C.c_int]
     lib.gq_strerror.restype = C.c_char_p
     lib.gq_version.argtypes = []
@@ -728,3 +753,221 @@ def gq_layer_norm_backward(a: gq_act, dy: torch.Tensor, x,
         _vec(weight, a.cols, "weight"), po, ldo, beta,
         _vec(dweight, a.cols, "dweight"), _vec(dbias, a.cols, "dbias"),
         pw, nw, _queue(stream, dy)), "gq_layer_norm_backward")
+
+
+# ------------------------------------------ 8-bit floating point ----
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+FP8_BLOCK = 128         # columns that share a step, and rows of a weight
+STATE_BLOCK = 256       # values of an 8-bit state that share a step
+
+
+def alloc_block(a: gq_act, device="cuda"):
+    """Device buffers of a form: (codes e4m3 [rows, pitch], steps fp32 [rows,
+    groups]) of a descriptor with group 128."""
+    return (torch.empty(a.rows, a.pitch, dtype=E4M3, device=device),
+            torch.empty(a.rows, a.groups, dtype=torch.float32, device=device))
+
+
+def alloc_block_weight(weight: gq_act, experts: int = 1, transposed: bool = False,
+                     device="cuda"):
+    """Device buffers of weights' forms: (codes [experts, out, pitch], steps
+    [experts, blocks of out, blocks of cols]), or of their transposes'."""
+    out, cols = weight.rows, weight.cols
+    if transposed:
+        out, cols = cols, out
+    return (torch.empty(experts, out, -(-cols // 16) * 16, dtype=E4M3, device=device),
+            torch.empty(experts, -(-out // FP8_BLOCK), -(-cols // FP8_BLOCK),
+                        dtype=torch.float32, device=device))
+
+
+def _block_form(codes, steps, a: gq_act, what: str):
+    return (_buffer(codes, E4M3, a.rows * a.pitch, what + " codes"),
+            _buffer(steps, torch.float32, a.rows * a.groups, what + " steps"))
+
+
+def _block_weight(form, experts: int, out: int, cols: int, what: str):
+    if form is None:
+        return None, None
+    codes, steps = form
+    blocks = -(-out // FP8_BLOCK) * -(-cols // FP8_BLOCK)
+    return (_buffer(codes, E4M3, experts * out * (-(-cols // 16) * 16), what + " codes"),
+            _buffer(steps, torch.float32, experts * blocks, what + " steps"))
+
+
+def _table(offsets):
+    """(pointer, experts) of an expert table; None: one expert, all rows."""
+    if offsets is None:
+        return None, 1
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets: a 1-D tensor of experts + 1 >= 2 entries")
+    return _ptr(offsets, torch.int64, "offsets"), offsets.numel() - 1
+
+
+def gq_block_pack(a: gq_act, x: torch.Tensor, codes: torch.Tensor,
+                steps: torch.Tensor, stream=None) -> None:
+    px, ld = _matrix(x, a, a.cols, "x")
+    pc, ps = _block_form(codes, steps, a, "x")
+    _check(_lib.gq_block_pack(a, px, ld, pc, ps, _queue(stream, x)), "gq_block_pack")
+
+
+def gq_block_unpack(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
+                  x: torch.Tensor, stream=None) -> None:
+    px, ld = _matrix(x, a, a.cols, "x")
+    pc, ps = _block_form(codes, steps, a, "x")
+    _check(_lib.gq_block_unpack(a, pc, ps, px, ld, _queue(stream, x)), "gq_block_unpack")
+
+
+def gq_block_pack_weight(weight: gq_act, w: torch.Tensor, form=None, t_form=None,
+                       stream=None) -> None:
+    """form, t_form: (codes, steps) that receive the form of w [(experts,) out,
+    cols] and of its transpose; weight: a descriptor of one expert's."""
+    if w.dim() not in (2, 3) or tuple(w.shape[-2:]) != (weight.rows, weight.cols):
+        raise ValueError(f"w: expected shape (experts, {weight.rows}, {weight.cols}), "
+                         f"got {tuple(w.shape)}")
+    experts = w.shape[0] if w.dim() == 3 else 1
+    pw = _buffer(w, weight.torch_dtype, 0, "w")
+    pc, ps = _block_weight(form, experts, weight.rows, weight.cols, "weight")
+    tc, ts = _block_weight(t_form, experts, weight.cols, weight.rows, "transposed weight")
+    _check(_lib.gq_block_pack_weight(weight, experts, pw, pc, ps, tc, ts,
+                                   _queue(stream, w)), "gq_block_pack_weight")
+
+
+def gq_block_linear_workspace(a: gq_act, out: int, experts: int = 1) -> int:
+    b = C.c_int64()
+    _check(_lib.gq_block_linear_workspace(a, out, experts, C.byref(b)),
+           "gq_block_linear_workspace")
+    return b.value
+
+
+def gq_block_linear(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
+                  w_codes: torch.Tensor, w_steps: torch.Tensor,
+                  bias: torch.Tensor | None, y: torch.Tensor,
+                  offsets: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> None:
+    """y [rows, out] <- x^ w^T + bias, by expert: offsets int64 [experts + 1]
+    on the device (None: one weight for all rows); codes and steps are the
+    input's form, w_codes and w_steps the weights'."""
+    if y.dim() != 2:
+        raise ValueError("y: expected a matrix")
+    out = y.shape[1]
+    po, experts = _table(offsets)
+    py, ld = _matrix(y, a, out, "y")
+    pc, ps = _block_form(codes, steps, a, "x")
+    wc, ws = _block_weight((w_codes, w_steps), experts, out, a.cols, "weight")
+    pw, nw = _space(workspace)
+    _check(_lib.gq_block_linear(a, out, experts, po, pc, ps, wc, ws,
+                              _vec(bias, experts * out, "bias"), py, ld, pw, nw,
+                              _queue(stream, y)), "gq_block_linear")
+
+
+def gq_block_wgrad_workspace(a: gq_act, out: int, experts: int = 1) -> int:
+    b = C.c_int64()
+    _check(_lib.gq_block_wgrad_workspace(a, out, experts, C.byref(b)),
+           "gq_block_wgrad_workspace")
+    return b.value
+
+
+def gq_block_wgrad(a: gq_act, dy: torch.Tensor, codes: torch.Tensor,
+                 steps: torch.Tensor, dweight: torch.Tensor,
+                 dbias: torch.Tensor | None = None,
+                 offsets: torch.Tensor | None = None, beta: float = 0.0,
+                 workspace: torch.Tensor | None = None, stream=None) -> None:
+    """dweight [experts * out * cols] <- beta * dweight + dy^T x^ of each
+    expert's rows, dbias [experts * out] <- beta * dbias + column sums of dy; dy
+    is [rows, out]."""
+    if dy.dim() != 2:
+        raise ValueError("dy: expected a matrix")
+    out = dy.shape[1]
+    po, experts = _table(offsets)
+    pd, ld = _matrix(dy, a, out, "dy")
+    pc, ps = _block_form(codes, steps, a, "x")
+    pw, nw = _space(workspace)
+    _check(_lib.gq_block_wgrad(a, out, experts, po, pd, ld, pc, ps, beta,
+                             _buffer(dweight, torch.float32, experts * out * a.cols,
+                                     "dweight"),
+                             _vec(dbias, experts * out, "dbias"), pw, nw,
+                             _queue(stream, dweight)), "gq_block_wgrad")
+
+
+# ------------------------------------------------- the optimizer's step ----
+def adamw(lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+          weight_decay: float = 0.0, bits: int = 32) -> gq_adamw_desc:
+    return gq_adamw_desc(lr, beta1, beta2, eps, weight_decay, bits)
+
+
+def alloc_adamw(d: gq_adamw_desc, n: int, device="cuda"):
+    """(m, v) of n parameters before the first step: fp32 [n] each, or with 8
+    bits (codes, steps) each."""
+    if d.bits == 32:
+        return torch.zeros(n, device=device), torch.zeros(n, device=device)
+
+    def state(kind):
+        return (torch.zeros(n, dtype=torch.uint8, device=device).view(kind),
+                torch.zeros(-(-n // STATE_BLOCK), device=device))
+    return state(E4M3), state(E5M2)
+
+
+def adamw_schedule(d: gq_adamw_desc, step: int, lr: float | None = None) -> torch.Tensor:
+    """The four words (on the host) that gq_adamw reads from ``schedule`` at
+    that step, to be copied to the device."""
+    w = torch.tensor([d.lr if lr is None else lr, 1 / (1 - d.beta1 ** step),
+                      (1 - d.beta2 ** step) ** -0.5, 0.0])
+    w.view(torch.int32)[3] = step - (1 << 32 if step >> 31 else 0)
+    return w
+
+
+def _state(s, bits: int, kind, n: int, what: str):
+    if bits == 32:
+        return _buffer(s, torch.float32, n, what), None
+    codes, steps = s
+    return (_buffer(codes, kind, n, what + " codes"),
+            _buffer(steps, torch.float32, -(-n // STATE_BLOCK), what + " steps"))
+
+
+def gq_adamw(d: gq_adamw_desc, g: torch.Tensor, p: torch.Tensor, m, v, step: int,
+             layer_offsets: torch.Tensor | None = None,
+             lr_scale: torch.Tensor | None = None,
+             decay: torch.Tensor | None = None,
+             grad_scale: torch.Tensor | None = None,
+             schedule: torch.Tensor | None = None,
+             p16: torch.Tensor | None = None, seed: int = 0, stream=None) -> None:
+    """One AdamW step of p (in place) from the gradient g; m and v as
+    alloc_adamw gives them; layer_offsets, lr_scale, decay: the layers' table,
+    learning rate factors and weight decays."""
+    n = p.numel()
+    if g.numel() != n:
+        raise ValueError("g must have p's size")
+    nl = 1
+    if layer_offsets is not None:
+        po, nl = _offsets(layer_offsets), layer_offsets.numel() - 1
+    else:
+        po = None
+    pm, sm = _state(m, d.bits, E4M3, n, "m")
+    pv, sv = _state(v, d.bits, E5M2, n, "v")
+    ph, kind = None, 0
+    if p16 is not None:
+        if p16.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"p16: expected a 16-bit type, got {p16.dtype}")
+        ph, kind = _buffer(p16, p16.dtype, n, "p16"), DTYPES[p16.dtype]
+    _check(_lib.gq_adamw(
+        d, n, nl, po, _vec(lr_scale, nl, "lr_scale"), _vec(decay, nl, "decay"),
+        _buffer(g, torch.float32, n, "g"), _vec(grad_scale, 1, "grad_scale"), step,
+        _vec(schedule, 4, "schedule"), _buffer(p, torch.float32, n, "p"), pm, sm, pv, sv,
+        ph, kind, seed, _queue(stream, p)), "gq_adamw")
+
+
+def gq_grad_norm_workspace(n: int) -> int:
+    b = C.c_int64()
+    _check(_lib.gq_grad_norm_workspace(n, C.byref(b)), "gq_grad_norm_workspace")
+    return b.value
+
+
+def gq_grad_norm(g: torch.Tensor, max_norm: float, norm: torch.Tensor | None,
+                 scale: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> None:
+    """norm [1] <- the gradient's norm, scale [1] <- the factor that clips it to
+    max_norm (gq_adamw's grad_scale)."""
+    pw, nw = _space(workspace)
+    _check(_lib.gq_grad_norm(
+        g.numel(), _buffer(g, torch.float32, 0, "g"), max_norm, _vec(norm, 1, "norm"),
+        _vec(scale, 1, "scale"), pw, nw, _queue(stream, g)), "gq_grad_norm")

@@ -444,6 +444,143 @@ int gq_layer_norm_backward(const gq_act* act, const void* dy, int64_t lddy,
                            float* dbias, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
+/* -------------------------------------------------------------------------
+ * The 8-bit floating point form, and the products of a training step on it.
+ * A matrix [rows, cols] is kept as
+ *   codes   e4m3 (OCP: 4 bits of exponent, 3 of mantissa, largest 448, no
+ *           infinity) [rows][pitch], pitch = cols rounded up to 16, codes past
+ *           the last column 0
+ *   steps   fp32 [rows][groups]: one per 128 consecutive columns of a row (the
+ *           last group may be short); act->group = 128 (GQ_EUNSUPPORTED
+ *           otherwise)
+ * with x^ = code * step.  step = 2^k, the smallest with 448 * step >= the
+ * group's largest |x| (at least 2^-126; at most 2^119, and 2^7 for fp16, where
+ * codes saturate and x^ stays finite); code = x / step rounded to the nearest
+ * e4m3 value, ties to even.  An all-zero group has step 0.  A group that holds a
+ * NaN or an infinity has step NaN and codes 0: it decodes as NaN, and its
+ * neighbours are untouched.  A form may also come from elsewhere: any codes (0
+ * past the last column; e4m3's NaN is one), and steps that are powers of two from
+ * 2^-126 to 2^127, 0 with codes 0, or NaN.  The products take a step's exponent
+ * alone.
+ *
+ * A weight [out, cols] has one step per block of 128 x 128:
+ *   codes [out][pitch of cols], steps [ceil(out / 128)][ceil(cols / 128)]
+ * by the same rules.  The form of its transpose is the transposed form: codes
+ * [cols][pitch of out], steps [ceil(cols / 128)][ceil(out / 128)], the same
+ * values, which is the weight of the product that gives the input's gradient.
+ *
+ * `experts` weights of the same size, one after the other, are used by the rows
+ * of a table: expert e has the rows [offsets[e], offsets[e + 1]) of the
+ * activations, offsets a DEVICE array of experts + 1 int64 values, 8-byte
+ * aligned, non-decreasing, within 0 .. rows (experts without rows are allowed,
+ * and so are rows before the first expert's and behind the last one's, which no
+ * call reads or writes).  offsets = NULL: one expert, all rows.  The table is not
+ * read on the host: other contents give unspecified outputs but never
+ * out-of-bounds accesses.  experts <= 1024 (GQ_EUNSUPPORTED beyond).
+ *
+ * Conventions: those of the 8-bit form above. */
+
+/* x -> form, and back (x <- x^ in act's type). */
+int gq_block_pack(const gq_act* act, const void* x, int64_t ldx, uint8_t* codes,
+                float* steps, void* stream);
+int gq_block_unpack(const gq_act* act, const uint8_t* codes, const float* steps,
+                  void* x, int64_t ldx, void* stream);
+
+/* Weights -> form, form of the transpose, or both in one pass (the pointers of
+ * the other are NULL).  weight: rows = out >= 1, cols, dtype of one expert's; w
+ * [experts][out][cols] contiguous, of the alignment of its elements. */
+int gq_block_pack_weight(const gq_act* weight, int32_t experts, const void* w,
+                       uint8_t* codes, float* steps, uint8_t* t_codes,
+                       float* t_steps, void* stream);
+
+/* Linear layer, by expert:
+ *   y[t, o] = sum_c x^[t, c] * w^[e(t), o, c] + bias[e(t), o]
+ * Products are exact; sums are fp32 and are rounded once to act's type.  codes,
+ * steps: the form of the input [rows, cols]; w_codes, w_steps: the experts'
+ * forms [out, cols] (for the input's gradient: of their transposes, with dy's
+ * form as input); bias fp32 [experts][out] or NULL.  y [rows, out], row stride
+ * ldy; rows of no expert are left as they are.  workspace:
+ * gq_block_linear_workspace bytes (may be NULL if that is 0).  GQ_EUNSUPPORTED for
+ * more than 2^24 tiles of 64 x 64 results. */
+int gq_block_linear_workspace(const gq_act* act, int64_t out, int32_t experts,
+                            int64_t* bytes);
+int gq_block_linear(const gq_act* act, int64_t out, int32_t experts,
+                  const int64_t* offsets, const uint8_t* codes,
+                  const float* steps, const uint8_t* w_codes,
+                  const float* w_steps, const float* bias, void* y, int64_t ldy,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Gradients of such a layer's weights and biases:
+ *   dweight[e, o, c] <- beta * dweight[e, o, c] + sum_{t of e} dy[t, o] * x^[t, c]
+ *   dbias[e, o]      <- beta * dbias[e, o]      + sum_{t of e} dy[t, o]
+ * dy [rows, out] in act's type, used as gq_act_wgrad uses it (fp32 in full);
+ * codes, steps: the form of the layer's input.  dweight fp32 [experts][out]
+ * [cols], dbias fp32 [experts][out] or NULL: slices of the flat gradient that
+ * gq_quantize takes.  An expert without rows gets beta times what was there.
+ * GQ_EUNSUPPORTED for more than 2^22 tiles of 128 x 128 results. */
+int gq_block_wgrad_workspace(const gq_act* act, int64_t out, int32_t experts,
+                           int64_t* bytes);
+int gq_block_wgrad(const gq_act* act, int64_t out, int32_t experts,
+                 const int64_t* offsets, const void* dy, int64_t lddy,
+                 const uint8_t* codes, const float* steps, float beta,
+                 float* dweight, float* dbias, void* workspace,
+                 int64_t workspace_bytes, void* stream);
+
+/* -------------------------------------------------------------------------
+ * The optimizer's step over all tensors at once: AdamW on the flat parameter
+ * vector, from the flat gradient that gq_dequantize_accumulate writes.
+ *   g' = grad_scale * g
+ *   m <- beta1 * m + (1 - beta1) * g',  v <- beta2 * v + (1 - beta2) * g'^2
+ *   p <- p - (lr_l / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *             + lr_l * decay_l * p)
+ * in fp32, with m and v as they are before they are stored.  Layer l = elements
+ * [layer_offsets[l], layer_offsets[l + 1]), a table as in gq_quantize_layers
+ * (NULL: nl = 1, one layer); lr_l = lr * lr_scale[l], decay_l = decay[l] (DEVICE
+ * fp32 [nl]; NULL: lr, and desc's weight_decay).
+ *
+ * bits = 32: m, v fp32 [n]; m_steps = v_steps = NULL.
+ * bits = 8: m e4m3 [n], v e5m2 [n] (OCP codes, v's sign is 0), each with fp32
+ * steps [ceil(n / 256)], one per 256 consecutive elements (whatever the
+ * layers): the smallest power of two with 448 * step >= the block's largest |m|
+ * (57344 for v), as in the form above.  Codes are rounded at random, so that
+ * the averages stay right in the mean: with f the place of the value between
+ * two neighbouring codes, cut to 16 bits, up iff f + u >= 1, u from Philox4x32-10
+ * with key = seed and counter = (i / 4, step); of word i mod 4 the upper 16 bits
+ * serve m, the lower 16 v.  v > 0 is never stored as 0.  All states start as
+ * zeros (codes and steps).
+ *
+ * grad_scale (DEVICE, one fp32, or NULL for 1): the factor of gq_grad_norm; if
+ * it is not finite the call changes nothing.  Otherwise a gradient that is not
+ * finite shows in its element, and with bits = 8 in its block of 256.
+ * step: 1 for the first call, at most 2^32 - 1.  schedule (or NULL): DEVICE,
+ * 16-byte aligned, {lr, 1 / (1 - beta1^step), 1 / sqrt(1 - beta2^step)} in fp32 and
+ * step as uint32, read by the kernel in place of desc->lr and step: a call that
+ * is captured into a graph is replayed with what they hold then.  p16 (or NULL)
+ * receives p in 16 bits (p16_dtype GQ_BF16 or GQ_F16).  Arrays that are written
+ * overlap no other. */
+typedef struct {
+  double lr, beta1, beta2; /* finite; 0 <= beta < 1                          */
+  double eps;              /* > 0 as an fp32 value                           */
+  double weight_decay;     /* finite                                         */
+  int32_t bits;            /* of a state's value: 32 or 8                    */
+} gq_adamw_desc;
+
+int gq_adamw(const gq_adamw_desc* desc, int64_t n, int32_t nl,
+             const int64_t* layer_offsets, const float* lr_scale,
+             const float* decay, const float* g, const float* grad_scale,
+             int64_t step, const float* schedule, float* p, void* m,
+             float* m_steps, void* v, float* v_steps, void* p16,
+             int32_t p16_dtype, uint64_t seed, void* stream);
+
+/* The gradient's norm, sqrt(sum g^2), and the factor that clips it: 1 up to
+ * max_norm (> 0, or infinity), max_norm / norm above, NaN if the norm is not
+ * finite.  Sums in 64 bits, in an order that only n decides.  norm, scale:
+ * DEVICE, one fp32 each; either may be NULL. */
+int gq_grad_norm_workspace(int64_t n, int64_t* bytes);
+int gq_grad_norm(int64_t n, const float* g, float max_norm, float* norm,
+                 float* scale, void* workspace, int64_t workspace_bytes,
+                 void* stream);
+
 /* Static description of a status code. */
 const char* gq_strerror(int status);
 

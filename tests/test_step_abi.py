@@ -1,0 +1,252 @@
+"""Refusals and sizes of the C entry points of the 8-bit floating point products
+and the optimizer's step: every argument error is found on the host before any
+launch (no GPU needed)."""
+import ctypes as C
+
+import pytest
+import torch
+
+M = 1 << 24                    # fake addresses, aligned and far apart
+
+
+@pytest.fixture(scope="module")
+def gq():
+    from communication_efficient_gradient_amd import gq as mod
+    return mod
+
+
+def act(gq, rows=10, cols=100, dtype=1, group=128):
+    return gq.gq_act(rows, cols, dtype, group)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), -1), (dict(cols=0), -1), (dict(cols=(1 << 20) + 1), -1),
+    (dict(rows=1 << 38), -1), (dict(dtype=3), -2), (dict(group=0), -2), (dict(group=64), -2),
+    (dict(group=100), -1)])
+def test_bad_descriptors(gq, kw, status):
+    L, a, b = gq.lib(), act(gq, **kw), C.c_int64()
+    assert L.gq_block_pack(a, M, 1 << 21, 2 * M, 3 * M, None) == status
+    assert L.gq_block_unpack(a, 2 * M, 3 * M, M, 1 << 21, None) == status
+    assert L.gq_block_pack_weight(a, 1, M, 2 * M, 3 * M, None, None, None) == status
+    assert L.gq_block_linear_workspace(a, 5, 1, C.byref(b)) == status
+    assert L.gq_block_wgrad_workspace(a, 5, 1, C.byref(b)) == status
+
+
+def test_pack_unpack_refusals(gq):
+    L, a = gq.lib(), act(gq)
+    for f, order in ((L.gq_block_pack, (0, 1, 2, 3)), (L.gq_block_unpack, (2, 3, 0, 1))):
+        def call(x=M, ld=100, codes=2 * M, steps=3 * M, desc=a):
+            v = [x, ld, codes, steps]
+            return f(desc, *[v[i] for i in order], None)
+        assert call(x=None) == -1
+        assert call(x=M + 1) == -1
+        assert call(ld=99) == -1
+        assert call(codes=None) == -1
+        assert call(codes=2 * M + 8) == -1
+        assert call(steps=None) == -1
+        assert call(steps=3 * M + 2) == -1
+        assert call(codes=M + 992) == -1               # inside x
+        assert call(x=2 * M + 1118) == -1              # codes' last bytes
+        assert call(x=None, codes=None, steps=None, desc=act(gq, rows=0)) == 0
+
+
+def test_pack_weight_refusals(gq):
+    L = gq.lib()
+
+    def call(w=M, c=2 * M, s=3 * M, tc=4 * M, ts=5 * M, experts=2, desc=act(gq, 50, 70)):
+        return L.gq_block_pack_weight(desc, experts, w, c, s, tc, ts, None)
+
+    assert call(experts=0) == -1
+    assert call(experts=1025) == -2
+    assert call(desc=act(gq, 0, 70)) == -1
+    assert call(desc=act(gq, (1 << 20) + 1, 70)) == -1
+    assert call(desc=act(gq, 1 << 18, 1 << 20), experts=2) == -1
+    assert call(w=None) == -1
+    assert call(w=M + 1) == -1
+    assert call(c=None, s=None, tc=None, ts=None) == -1
+    assert call(c=None) == -1
+    assert call(ts=None) == -1
+    assert call(c=2 * M + 8) == -1
+    assert call(tc=2 * M + 16) == -1                   # inside the other form
+    assert call(c=M + 50 * 70 * 2 * 2 - 4) == -1       # w's last values (16-byte aligned or not)
+    assert call(s=M + 64) == -1
+
+
+def test_linear_refusals(gq):
+    L = gq.lib()
+
+    def call(out=50, experts=3, off=9 * M, codes=M, steps=2 * M, wc=3 * M, ws=4 * M, bias=5 * M,
+             y=6 * M, ld=50, work=7 * M, nb=None, desc=act(gq)):
+        need = C.c_int64()
+        if nb is None:
+            L.gq_block_linear_workspace(desc, out, experts, C.byref(need))
+            nb = need.value
+        return L.gq_block_linear(desc, out, experts, off, codes, steps, wc, ws, bias, y, ld, work,
+                               nb, None)
+
+    assert call(out=0) == -1
+    assert call(out=(1 << 20) + 1) == -1
+    assert call(experts=0) == -1
+    assert call(experts=1025) == -2
+    assert call(off=None) == -1                        # several experts need a table
+    assert call(off=9 * M + 4) == -1
+    assert call(desc=act(gq, rows=1 << 31, cols=1), out=64, nb=1 << 40) == -2  # too many tiles
+    assert call(codes=None) == -1
+    assert call(steps=None) == -1
+    assert call(wc=None) == -1
+    assert call(wc=3 * M + 4) == -1
+    assert call(ws=None) == -1
+    assert call(bias=5 * M + 1) == -1
+    assert call(y=None) == -1
+    assert call(ld=49) == -1
+    assert call(y=3 * M + 3 * 50 * 112 - 2) == -1      # over the last weight's last code
+    assert call(y=5 * M + 4 * 149) == -1               # over the biases' last value
+    assert call(y=9 * M + 24) == -1                    # over the table
+    big = dict(desc=act(gq, rows=1100, cols=60000), out=1000, experts=1, off=None, ld=1000,
+               codes=M, steps=8 * M, wc=10 * M, ws=15 * M, bias=16 * M, y=17 * M, work=18 * M)
+    need = C.c_int64()
+    assert L.gq_block_linear_workspace(big["desc"], 1000, 1, C.byref(need)) == 0
+    assert need.value > 0
+    assert call(**big, nb=need.value - 1) == -1
+    assert call(**{**big, "work": None}) == -1
+    assert call(**{**big, "work": 18 * M + 8}) == -1
+    assert call(**{**big, "work": M}) == -1            # over the codes
+    assert call(desc=act(gq, rows=0), codes=None, steps=None, y=None) == 0
+    assert L.gq_block_linear_workspace(act(gq), 50, 1, None) == -1
+
+
+def test_wgrad_refusals(gq):
+    L = gq.lib()
+
+    def call(out=50, experts=3, off=9 * M, dy=M, ld=50, codes=2 * M, steps=3 * M, beta=0.0,
+             dw=4 * M, db=5 * M, work=6 * M, nb=None, desc=act(gq)):
+        need = C.c_int64()
+        if nb is None:
+            L.gq_block_wgrad_workspace(desc, out, experts, C.byref(need))
+            nb = need.value
+        return L.gq_block_wgrad(desc, out, experts, off, dy, ld, codes, steps, beta, dw, db, work,
+                              nb, None)
+
+    assert call(out=0) == -1
+    assert call(experts=0) == -1
+    assert call(experts=1025) == -2
+    assert call(off=None) == -1
+    assert call(off=9 * M + 4) == -1
+    assert call(dy=None) == -1
+    assert call(dy=M + 1) == -1
+    assert call(ld=49) == -1
+    assert call(codes=2 * M + 8) == -1
+    assert call(steps=None) == -1
+    assert call(beta=float("nan")) == -1
+    assert call(dw=None) == -1
+    assert call(dw=4 * M + 2) == -1
+    assert call(db=5 * M + 2) == -1
+    assert call(dw=M + 64) == -1                       # over dy
+    assert call(db=4 * M + 4 * (3 * 5000 - 1)) == -1   # over the last weight's last gradient
+    assert call(dw=9 * M + 24) == -1                   # over the table
+    long = act(gq, rows=100000)
+    need = C.c_int64()
+    assert L.gq_block_wgrad_workspace(long, 50, 3, C.byref(need)) == 0
+    assert need.value > 0
+    assert call(desc=long, nb=need.value - 1) == -1
+    assert call(desc=long, work=None) == -1
+    assert call(desc=long, work=2 * M) == -1
+    assert L.gq_block_wgrad_workspace(act(gq, cols=1 << 20), 1 << 16, 4, C.byref(need)) == -2
+
+
+def test_adamw_refusals(gq):
+    L = gq.lib()
+    good = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1, bits=8)
+
+    def call(desc=good, n=1000, nl=3, off=M, rate=2 * M, decay=3 * M, g=4 * M, scale=5 * M, step=1,
+             sched=6 * M, p=7 * M, m=8 * M, ms=9 * M, v=10 * M, vs=11 * M, p16=12 * M, kind=1):
+        d = None if desc is None else gq.adamw(**desc)
+        return L.gq_adamw(d, n, nl, off, rate, decay, g, scale, step, sched, p, m, ms, v, vs, p16,
+                          kind, 0, None)
+
+    nan, inf = float("nan"), float("inf")
+    assert call(desc=None) == -1
+    for k, bad in (("lr", (nan, inf)), ("beta1", (-0.1, 1.0, nan)), ("beta2", (-0.1, 1.0, nan)),
+                   ("eps", (0.0, -1.0, nan, inf, 1e-60, 1e60)), ("weight_decay", (nan, inf))):
+        for b in bad:
+            assert call(desc={**good, k: b}) == -1
+    assert call(desc={**good, "bits": 16}) == -2
+    assert call(n=0) == -1
+    assert call(nl=0) == -1
+    assert call(off=None) == -1                        # several layers need a table
+    assert call(off=M + 4) == -1
+    assert call(step=0) == -1
+    assert call(step=1 << 32) == -1
+    assert call(rate=2 * M + 2) == -1
+    assert call(decay=3 * M + 2) == -1
+    assert call(scale=5 * M + 2) == -1
+    assert call(sched=6 * M + 8) == -1
+    for k in ("g", "p", "m", "v"):
+        assert call(**{k: None}) == -1
+        assert call(**{k: 20 * M + 8}) == -1
+    assert call(ms=None) == -1
+    assert call(vs=11 * M + 2) == -1
+    assert call(p16=12 * M + 8) == -1
+    assert call(kind=0) == -2
+    assert call(desc={**good, "bits": 32}) == -1       # fp32 states have no steps
+    assert call(p=4 * M + 3984) == -1                  # over the gradient's last values
+    assert call(m=10 * M + 992) == -1                  # over v
+    assert call(ms=10 * M + 996) == -1
+    assert call(desc={**good, "bits": 32}, ms=None, vs=None, m=10 * M + 3984) == -1
+    assert call(p16=7 * M + 16) == -1
+    assert call(v=M + 16) == -1                        # over the table
+    assert call(vs=5 * M) == -1
+
+
+def test_norm_refusals(gq):
+    L = gq.lib()
+    need = C.c_int64()
+    assert L.gq_grad_norm_workspace(0, C.byref(need)) == -1
+    assert L.gq_grad_norm_workspace(10, None) == -1
+    assert L.gq_grad_norm_workspace(1 << 20, C.byref(need)) == 0 and need.value > 0
+
+    def call(n=1 << 20, g=M, most=1.0, norm=2 * M, scale=3 * M, work=4 * M, nb=None):
+        return L.gq_grad_norm(n, g, most, norm, scale, work, need.value if nb is None else nb, None)
+
+    assert call(n=0) == -1
+    assert call(g=None) == -1
+    assert call(g=M + 8) == -1
+    for bad in (0.0, -1.0, float("nan")):
+        assert call(most=bad) == -1
+    assert call(norm=None, scale=None) == -1
+    assert call(norm=2 * M + 2) == -1
+    assert call(work=None) == -1
+    assert call(nb=need.value - 1) == -1
+    assert call(norm=M + 4) == -1
+    assert call(scale=4 * M + 4) == -1
+
+
+def test_binding_checks(gq):
+    a = gq.act(4, 6, torch.bfloat16, 128)
+    host = torch.zeros(4, 6, dtype=torch.bfloat16)
+    codes, steps = gq.alloc_block(a, device="cpu")
+    assert codes.shape == (4, 16) and steps.shape == (4, 1)
+    with pytest.raises(ValueError, match="device tensor"):
+        gq.gq_block_pack(a, host, codes, steps)
+    with pytest.raises(ValueError, match="matrix"):
+        gq.gq_block_linear(a, codes, steps, codes, steps, None, host[0])
+    with pytest.raises(ValueError, match="offsets"):
+        gq.gq_block_linear(a, codes, steps, codes, steps, None, host,
+                         offsets=torch.zeros(1, dtype=torch.int64))
+    with pytest.raises(ValueError, match="expected shape"):
+        gq.gq_block_pack_weight(gq.act(6, 4, torch.bfloat16, 128), host)
+    with pytest.raises(gq.GQError) as ex:
+        gq.gq_block_linear_workspace(gq.act(4, 64, torch.float32, 64), 8)
+    assert ex.value.status == gq.GQ_EUNSUPPORTED
+    w = gq.act(130, 200, torch.float32, 128)
+    c, s = gq.alloc_block_weight(w, 3, device="cpu")
+    assert c.shape == (3, 130, 208) and s.shape == (3, 2, 2)
+    c, s = gq.alloc_block_weight(w, 3, transposed=True, device="cpu")
+    assert c.shape == (3, 200, 144) and s.shape == (3, 2, 2)
+    m, v = gq.alloc_adamw(gq.adamw(1e-3, bits=8), 257, device="cpu")
+    assert m[0].dtype == torch.float8_e4m3fn and v[0].dtype == torch.float8_e5m2
+    assert m[1].shape == v[1].shape == (2,)
+    with pytest.raises(ValueError, match="size"):
+        gq.gq_adamw(gq.adamw(1e-3), torch.zeros(3), torch.zeros(4), None, None, 1)
+    w = gq.adamw_schedule(gq.adamw(0.5, 0.9, 0.99), 2 ** 32 - 1, lr=0.25)
+    assert w.tolist()[:3] == [0.25, 1.0, 1.0] and w.view(torch.int32)[3] == -1
