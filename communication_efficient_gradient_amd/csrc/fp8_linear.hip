@@ -194,15 +194,19 @@ __device__ __forceinline__ f32x4 product(i32x8 a, i32x8 b, f32x4 c, uint32_t sa,
 // Tiles of BM tokens by BN outputs, WM by WN of one per wave, in k-tiles of
 // 128 codes, which is one step.  An LDS row is 128 bytes in eight 16-byte
 // chunks, chunk j of row r at place j ^ (r / 2 % 8): sixteen lanes that read
-// one chunk of sixteen rows then touch every bank once.  NS k-tiles share LDS:
-// one is multiplied while NS - 1 are on their way.  Workgroups stay and walk
-// the tiles, and the copies run on into the next tile.
+// one chunk of sixteen rows then touch every bank once.  The steps of the rows
+// and of the weight's blocks lie behind the codes.  NS k-tiles share LDS: one
+// is multiplied while NS - 1 are on their way.  Workgroups stay and walk the
+// tiles, and the copies run on into the next tile while the present one's last
+// products run and its results leave.
 template <typename T, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(LinearArgs a) {
-  constexpr int BK = 128, CH = BK / 16, KK = BK / 64, RPI = 64 / CH;
+  constexpr bool EXACT = std::is_same_v<T, float>;
+  constexpr int BK = 128, CH = BK / 16, RPI = 64 / CH;
   constexpr int WAVES = (BM / WM) * (BN / WN);
   constexpr int MT = WM / 32, NTL = WN / 32;
-  constexpr int BUF = (BM + BN) * BK;
+  constexpr int CODES = (BM + BN) * BK, BUF = CODES + (BM + 64) * 4;
+  static_assert(BM / 64 < WAVES, "a wave for the weight's steps");
   __shared__ __attribute__((aligned(16))) uint8_t lds[NS * BUF];
   __shared__ Experts experts;
   const int lane = (int)threadIdx.x & 63;
@@ -210,18 +214,28 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
   read_experts<BM>(a, experts);
 
-  // copies: a wave instruction fills RPI rows.  Rows past the end lie behind
-  // the buffers' ranges and read as zeros.
-  constexpr int CM = BM / RPI / WAVES, CN = BN / RPI / WAVES;
+  // copies: a wave instruction fills RPI rows of codes; one more brings the
+  // steps of 64 rows, or of the weight (the waves past those).  Rows past the
+  // end lie behind the buffers' ranges and read as zeros.
+  constexpr int CM = BM / RPI / WAVES, CN = BN / RPI / WAVES, COPIES = CM + CN + 1;
   const int cl = lane % CH, rl = lane / CH;
-  BufferRange bm, bn;
+  const bool row_steps = wave < BM / 64;
+  const int step_at = row_steps ? (wave * 64 + lane) * a.groups * 4
+                                : min(lane, (BN - 1) / kFp8Block) * a.groups * 4;
+  const int step_to = CODES + (row_steps ? wave * 256 : BM * 4);
+  BufferRange bm, bn, bs;
   auto ranges_of = [&](const ExpertTile& t) {
-    const int n = t.j * BN;
+    const int n = t.j * BN, rows = min(t.end - t.row, BM);
     // of this tile's rows only: shorter than kPastEnd whatever the matrix
-    bm = range_of(a.codes + (int64_t)t.row * a.pitch,
-                  (int64_t)min(t.end - t.row, BM) * a.pitch);
+    bm = range_of(a.codes + (int64_t)t.row * a.pitch, (int64_t)rows * a.pitch);
     bn = range_of(a.w_codes + ((int64_t)t.expert * a.out + n) * a.pitch,
                   (int64_t)min(a.out - n, BN) * a.pitch);
+    const int blocks = div_up(a.out, kFp8Block), block = n / kFp8Block;
+    bs = row_steps
+             ? range_of(a.steps + (int64_t)t.row * a.groups, (int64_t)rows * a.groups * 4)
+             : range_of(a.w_steps + ((int64_t)t.expert * blocks + block) * a.groups,
+                        (int64_t)min(blocks - block, (BN + kFp8Block - 1) / kFp8Block) *
+                            a.groups * 4);
   };
   const int k_tiles = a.groups;
   // what is copied next: k-tile ck (up to cend) of the walk's last tile, into cat
@@ -251,6 +265,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       copy16_to_lds(bn, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
                     (LdsPtr)&lds[cat + BM * BK + (wave * CN + i) * 1024]);
     }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(bs, (LdsPtr)&lds[cat + step_to], 4, step_at, ck * 4,
+                                             0, 0);
     cat = cat + BUF == NS * BUF ? 0 : cat + BUF;
     if (++ck == cend) {
       copying = copies.take<BM>(&ctile);
@@ -259,22 +275,26 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   };
   // Waits until this wave's reads are done and its copies but those of the NS -
   // 2 youngest k-tiles have arrived, then for the other waves.  Copies arrive
-  // in order; anything else in flight only makes the wait longer.  Once there
-  // is nothing left to copy the youngest are fewer, so all are waited for.
+  // in order; anything else in flight (results on their way out) only makes
+  // the wait longer.  Once there is nothing left to copy the youngest are
+  // fewer, so all are waited for.
   auto meet = [&](bool all) {
     if (NS == 2 || all) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     } else {
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * (CM + CN)) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((NS - 2) * COPIES) : "memory");
     }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
 
+  // Fragments: 32 rows by 64 codes.  Those of the next half k-tile are read
+  // between the present one's products (the scheduling groups), a token's as
+  // soon as its last product is on its way.
   const int fr = lane % 32;
-  int place[KK][2];
+  int place[2][2];
 #pragma unroll
-  for (int kk = 0; kk < KK; ++kk)
+  for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       place[kk][h] = fr * BK + (((kk * 4 + lane / 32 * 2 + h) ^ (fr / 2 % CH)) << 4);
@@ -282,6 +302,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
     const i32x4 lo = *reinterpret_cast<const i32x4*>(&lds[at + row * BK + place[kk][0]]);
     const i32x4 hi = *reinterpret_cast<const i32x4*>(&lds[at + row * BK + place[kk][1]]);
     return join16(lo, hi);
+  };
+  i32x8 fm[MT], fn[2][NTL];
+  uint32_t em[2][MT], en[2];      // the steps, of this k-tile and the next
+  auto read_n = [&](int to, int at, int kk) {
+#pragma unroll
+    for (int i = 0; i < NTL; ++i) fn[to][i] = fragment(at + BM * BK, wn + i * 32, kk);
+  };
+  auto read_steps = [&](int to, int at) {
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      em[to][j] = *reinterpret_cast<const uint32_t*>(&lds[at + CODES + (wm + j * 32 + fr) * 4]);
+    en[to] = *reinterpret_cast<const uint32_t*>(
+        &lds[at + CODES + (BM + (BN > kFp8Block ? wn / kFp8Block : 0)) * 4]);
   };
 
   ExpertWalk walk(experts, a.experts, a.ntiles, a.splits);
@@ -292,16 +325,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   for (int i = 0; i < NS - 1; ++i) copy_next();
   meet(!copying);
   int at = 0;
+  read_steps(0, 0);
+  read_n(0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < MT; ++j) fm[j] = fragment(0, wm + j * 32, 0);
   for (;;) {
     const int n0 = tile.j * BN;
     const int first = tile.split * a.per, last = min(first + a.per, k_tiles);
-    // steps: of the lane's token in each 32 x 32 tile, and of the weight's block
-    const BufferRange sm = range_of(a.steps + (int64_t)tile.row * a.groups,
-                                    (int64_t)min(tile.end - tile.row, BM) * a.groups * 4);
-    const BufferRange sn = range_of(
-        a.w_steps + ((int64_t)tile.expert * div_up(a.out, kFp8Block) + n0 / kFp8Block) * a.groups,
-        (int64_t)(BN > kFp8Block ? min(BN / kFp8Block, div_up(a.out - n0, kFp8Block)) : 1) *
-            a.groups * 4);
     f32x16 acc[NTL][MT];
 #pragma unroll
     for (int i = 0; i < NTL; ++i)
@@ -312,29 +342,34 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
     int was = at;
     for (int kt = first; kt < last; ++kt) {
       was = at;
-      uint32_t em[MT];
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-        em[j] = __builtin_amdgcn_raw_buffer_load_b32(
-            sm, ((wm + j * 32 + fr) * a.groups + kt) * 4, 0, 0);
-      const uint32_t en = __builtin_amdgcn_raw_buffer_load_b32(
-          sn, ((BN > kFp8Block ? wn / kFp8Block : 0) * a.groups + kt) * 4, 0, 0);
       copy_next();
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        i32x8 fm[MT], fn[NTL];
+      for (int kk = 0; kk < 2; ++kk) {
+        if (kk == 1) {
+          meet(!copying);  // the next k-tile is in LDS, this one is read
+          at = at + BUF == NS * BUF ? 0 : at + BUF;
+          read_steps(1, at);
+        }
+        read_n(1 - kk, at, 1 - kk);
 #pragma unroll
-        for (int i = 0; i < NTL; ++i) fn[i] = fragment(at + BM * BK, wn + i * 32, kk);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) fm[j] = fragment(at, wm + j * 32, kk);
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
+        for (int j = 0; j < MT; ++j) {
 #pragma unroll
           for (int i = 0; i < NTL; ++i)
-            acc[i][j] = product<std::is_same_v<T, float>>(fn[i], fm[j], acc[i][j], en, em[j]);
+            acc[i][j] = product<EXACT>(fn[kk][i], fm[j], acc[i][j], en[0], em[0][j]);
+          fm[j] = fragment(at, wm + j * 32, 1 - kk);
+        }
+        if constexpr (!EXACT) {
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            __builtin_amdgcn_sched_group_barrier(0x008, NTL, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 + (2 * NTL + MT - 1) / MT, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      meet(!copying);  // the next k-tile is in LDS, this one is read
-      at = at + BUF == NS * BUF ? 0 : at + BUF;
+#pragma unroll
+      for (int j = 0; j < MT; ++j) em[0][j] = em[1][j];
+      en[0] = en[1];
     }
     // A lane holds, of one token per 32 x 32 tile, four consecutive outputs in
     // each of the tile's four quarters: eight bytes of bf16, at 32 rows of y.
@@ -344,7 +379,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
     if (a.splits == 1) {
       using V = typename Word16<T>::V;  // 16 bytes of results
       constexpr int E = 16 / (int)sizeof(T), ROW = WN / E;  // pieces per row
-      constexpr int MINE = BUF / WAVES, FIT = MINE / (WN * (int)sizeof(T));
+      constexpr int MINE = CODES / WAVES, FIT = MINE / (WN * (int)sizeof(T));
       constexpr int TOK = FIT < WM ? FIT : WM;
       static_assert(TOK % 32 == 0 && WM % TOK == 0, "");
       uint8_t* mine = lds + was + wave * MINE;
