@@ -212,9 +212,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   // slots as k-tiles, since each may be the first of another tile
   constexpr int BLOCKS = (BN + kFp8Block - 1) / kFp8Block, SLOT = (BM + 2) * 16;
   static_assert(BM / 64 < WAVES && BLOCKS <= 2, "a wave for the weight's steps");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * BUF];
-  __shared__ __attribute__((aligned(16))) uint8_t steps[NS * SLOT];
-  __shared__ Experts experts;
+  // One array: with several the compiler tells them apart, and waits for all
+  // copies before it reads from one that they may go to.
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * (BUF + SLOT) + sizeof(Experts)];
+  constexpr int STEPS = NS * BUF;
+  Experts& experts = *reinterpret_cast<Experts*>(&lds[NS * (BUF + SLOT)]);
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
@@ -272,7 +274,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
     if (ck == csteps) {
       // what lies past a row's last step is not used
       if (row_steps || (wave == BM / 64 && lane < BLOCKS))
-        copy16_to_lds(bs, step_at, ck * 4, (LdsPtr)&steps[csat + step_to]);
+        copy16_to_lds(bs, step_at, ck * 4, (LdsPtr)&lds[STEPS + csat + step_to]);
       csteps += 4;
       csat = csat + SLOT == NS * SLOT ? 0 : csat + SLOT;
     }
@@ -299,8 +301,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   };
 
   // Fragments: 32 rows by 64 codes.  Those of the next half k-tile are read
-  // between the present one's products (the scheduling groups), a token's as
-  // soon as its last product is on its way.
+  // between the present one's products, a token's as soon as its last product
+  // is on its way and into the same registers (the scheduling barriers: all at
+  // once they would need 32 more than there are).
   const int fr = lane % 32;
   int place[2][2];
 #pragma unroll
@@ -308,24 +311,28 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       place[kk][h] = fr * BK + (((kk * 4 + lane / 32 * 2 + h) ^ (fr / 2 % CH)) << 4);
-  auto fragment = [&](int at, int row, int kk) {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(&lds[at + row * BK + place[kk][0]]);
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(&lds[at + row * BK + place[kk][1]]);
-    return join16(lo, hi);
+  auto half = [&](int at, int row, int kk, int h) {
+    return *reinterpret_cast<const i32x4*>(&lds[at + row * BK + place[kk][h]]);
   };
-  i32x8 fm[MT], fn[2][NTL];
+  i32x4 fm[MT][2], fn[2][NTL][2];
   uint32_t em[2][MT], en[2];      // the steps, of this k-tile and the next
-  auto read_n = [&](int to, int at, int kk) {
+  auto read_m = [&](int j, int at, int kk) {
 #pragma unroll
-    for (int i = 0; i < NTL; ++i) fn[to][i] = fragment(at + BM * BK, wn + i * 32, kk);
+    for (int h = 0; h < 2; ++h) fm[j][h] = half(at, wm + j * 32, kk, h);
+  };
+  // the j-th of MT parts of the weight's
+  auto read_n = [&](int j, int to, int at, int kk) {
+#pragma unroll
+    for (int i = j * 2 * NTL / MT; i < (j + 1) * 2 * NTL / MT; ++i)
+      fn[to][i / 2][i % 2] = half(at + BM * BK, wn + i / 2 * 32, kk, i % 2);
   };
   int sat = 0;                    // where the steps of the next k-tile lie
   auto read_steps = [&](int to) {
 #pragma unroll
     for (int j = 0; j < MT; ++j)
-      em[to][j] = *reinterpret_cast<const uint32_t*>(&steps[sat + (wm + j * 32 + fr) * 16]);
+      em[to][j] = *reinterpret_cast<const uint32_t*>(&lds[STEPS + sat + (wm + j * 32 + fr) * 16]);
     en[to] = *reinterpret_cast<const uint32_t*>(
-        &steps[sat + (BM + (BN > kFp8Block ? wn / kFp8Block : 0)) * 16]);
+        &lds[STEPS + sat + (BM + (BN > kFp8Block ? wn / kFp8Block : 0)) * 16]);
   };
   // on to the next k-tile's, `k` of them behind the tile's first
   auto next_steps = [&](int k) {
@@ -342,9 +349,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   meet(std::integral_constant<int, NS - 1>{}, !copying);
   int at = 0;
   read_steps(0);
-  read_n(0, 0, 0);
 #pragma unroll
-  for (int j = 0; j < MT; ++j) fm[j] = fragment(0, wm + j * 32, 0);
+  for (int j = 0; j < MT; ++j) {
+    read_m(j, 0, 0);
+    read_n(j, 0, 0, 0);
+  }
   for (;;) {
     const int n0 = tile.j * BN;
     const int first = tile.split * a.per, last = min(first + a.per, k_tiles);
@@ -361,6 +370,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         if (kk == 1) {
+          // keeps the first half's products before the barrier: the compiler
+          // would move them behind the copies' branches, to the others
+#pragma unroll
+          for (int i = 0; i < NTL; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[i][j]));
           // the next k-tile is in LDS and this one is read: its place is free,
           // but for the last one's, through which the results leave first
           meet(std::integral_constant<int, NS - 2>{}, !copying);
@@ -369,22 +384,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
           next_steps(kt + 1 == last ? 0 : kt + 1 - first);
           read_steps(1);
         }
-        read_n(1 - kk, at, 1 - kk);
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
 #pragma unroll
           for (int i = 0; i < NTL; ++i)
-            acc[i][j] = product<EXACT>(fn[kk][i], fm[j], acc[i][j], en[0], em[0][j]);
-          fm[j] = fragment(at, wm + j * 32, 1 - kk);
+            acc[i][j] = product<EXACT>(join16(fn[kk][i][0], fn[kk][i][1]),
+                                       join16(fm[j][0], fm[j][1]), acc[i][j], en[0], em[0][j]);
+          read_m(j, at, 1 - kk);
+          read_n(j, 1 - kk, at, 1 - kk);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (!EXACT) {
-#pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            __builtin_amdgcn_sched_group_barrier(0x008, NTL, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2 + (2 * NTL + MT - 1) / MT, 0);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int j = 0; j < MT; ++j) em[0][j] = em[1][j];
@@ -491,6 +500,132 @@ __global__ __launch_bounds__(256) void k_fp8_linear_join(LinearArgs a) {
   }
 }
 
+// Few tokens.  A workgroup takes 16 * MT tokens of an expert by 16 * NT outputs
+// (16 * MT more behind them, if there are); its eight waves take turns of four
+// k-tiles along the sum and add up in LDS.  Operands come straight from memory
+// and L2 in the products' layout, 32 codes of one row per lane, 16 rows by 128
+// codes per instruction: nothing waits for a barrier until the sums are joined.
+constexpr int kFewWaves = 8;
+
+template <typename T, int MT, int NT>
+__global__ __launch_bounds__(kFewWaves * 64) void k_fp8_linear_few(LinearArgs a) {
+  constexpr bool EXACT = std::is_same_v<T, float>;
+  constexpr int U = 4, HALF = kFewWaves / 2, E = MT * NT * 256;
+  __shared__ __attribute__((aligned(16))) float sums[HALF][E];
+  const int lane = (int)threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int n0 = (int)blockIdx.x * (16 * NT), expert = (int)blockIdx.y;
+  const Tokens t = tokens_of(a.offsets, expert, a.rows);
+  const int blocks = div_up(a.out, kFp8Block);
+  const BufferRange w = range_of(a.w_codes + ((int64_t)expert * a.out + n0) * a.pitch,
+                                 (int64_t)min(a.out - n0, 16 * NT) * a.pitch);
+  // 16 * NT outputs lie in one block
+  const BufferRange sw =
+      range_of(a.w_steps + ((int64_t)expert * blocks + n0 / kFp8Block) * a.groups,
+               (int64_t)a.groups * 4);
+  const float* bias = a.bias ? a.bias + (int64_t)expert * a.out : nullptr;
+  const int row = lane % 16 * a.pitch, col = lane / 16 * 32;
+  for (int64_t m0 = t.lo + (int64_t)blockIdx.z * (16 * MT); m0 < t.hi;
+       m0 += (int64_t)gridDim.z * (16 * MT)) {
+    const int64_t rows = min(t.hi - m0, (int64_t)(16 * MT));
+    const BufferRange x = range_of(a.codes + m0 * a.pitch, rows * a.pitch);
+    const BufferRange sx = range_of(a.steps + m0 * a.groups, rows * a.groups * 4);
+    f32x4 acc[NT][MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = wave * U; k < a.groups; k += kFewWaves * U) {
+      i32x8 fw[U][NT], fx[U][MT];
+      u32x4 ew, ex[MT];
+      auto load = [&](const BufferRange& r, int c, int at) {
+        // past the pitch lies the next row: those chunks are zeros
+        const i32x4 lo = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, c < a.pitch ? at + c : kPastEnd, 0, 0));
+        const i32x4 hi = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       r, c + 16 < a.pitch ? at + c + 16 : kPastEnd, 0, 0));
+        return join16(lo, hi);
+      };
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = (k + u) * 128 + col;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fw[u][j] = load(w, c, row + j * 16 * a.pitch);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) fx[u][i] = load(x, c, row + i * 16 * a.pitch);
+      }
+      ew = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(sw, k * 4, 0, 0));
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        ex[i] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       sx, ((lane % 16 + i * 16) * a.groups + k) * 4, 0, 0));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k + u >= a.groups) break;   // there lie other rows' steps
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[j][i] = product<EXACT>(fw[u][j], fx[u][i], acc[j][i], ew[u], ex[i][u]);
+      }
+    }
+    // a lane holds four consecutive outputs of token lane % 16; kept as
+    // [token][output], 16 * NT outputs to a token
+    auto at = [&](int j, int i) {
+      return (i * 16 + lane % 16) * (16 * NT) + j * 16 + lane / 16 * 4;
+    };
+    if (wave >= HALF) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          *reinterpret_cast<f32x4*>(&sums[wave - HALF][at(j, i)]) = acc[j][i];
+    }
+    __syncthreads();
+    if (wave < HALF) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          f32x4* p = reinterpret_cast<f32x4*>(&sums[wave][at(j, i)]);
+          *p += acc[j][i];
+        }
+    }
+    __syncthreads();
+    for (int e = (int)threadIdx.x * 4; e < E; e += kFewWaves * 64 * 4) {
+      const int64_t m = m0 + e / (16 * NT);
+      const int n = n0 + e % (16 * NT);
+      if (m >= t.hi || n >= a.out) continue;
+      f32x4 s = *reinterpret_cast<const f32x4*>(&sums[0][e]);
+#pragma unroll
+      for (int v = 1; v < HALF; ++v) s += *reinterpret_cast<const f32x4*>(&sums[v][e]);
+      T o[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = (T)(s[r] + (bias ? bias[min(n + r, a.out - 1)] : 0.f));
+      T* y = (T*)a.y + m * a.ldy + n;
+      if (n + 4 <= a.out) {
+        __builtin_memcpy(y, o, sizeof(o));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < a.out) y[r] = o[r];
+      }
+    }
+    __syncthreads();   // the sums are read
+  }
+}
+
+bool few_tokens(const ActDims& A, int64_t out, int experts) { return A.rows <= 64; }
+
+template <typename T, int MT, int NT>
+void few(const LinearArgs& a, int most, hipStream_t st) {
+  const int z = div_up(a.rows, 16 * MT);
+  const dim3 g(div_up(a.out, 16 * NT), a.experts, z < most ? z : most);
+  k_fp8_linear_few<T, MT, NT><<<g, kFewWaves * 64, 0, st>>>(a);
+}
+
 struct Plan {
   int splits, per;  // of the sum, and 128-byte k-tiles of one
   int tile;         // rows and columns of a tile
@@ -499,13 +634,14 @@ struct Plan {
 Plan plan_linear(const ActDims& A, int64_t out, int experts) {
   const int kt = A.groups;
   Plan best = {1, kt, 0};
+  if (few_tokens(A, out, experts)) return best;
   double least = 1e30;
   // as if the tokens were spread evenly over the experts
   const int64_t each = (A.rows + experts - 1) / experts;
   const int64_t used = (A.rows + each - 1) / each;
   for (int tile = 64; tile <= 256; tile *= 2) {
     const int64_t tiles = used * ((each + tile - 1) / tile) * ((out + tile - 1) / tile);
-    for (int s = 1; s <= 8 && (s == 1 || (A.rows > 64 && kt / s >= 8)); ++s) {
+    for (int s = 1; s <= 8 && (s == 1 || kt / s >= 8); ++s) {
       const int per = div_up(kt, s);
       const int64_t groups = tiles * s;
       const double rounds = (double)((groups + kCus - 1) / kCus);
@@ -526,6 +662,12 @@ Plan plan_linear(const ActDims& A, int64_t out, int experts) {
 
 template <typename T>
 int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
+  if (few_tokens(A, a.out, a.experts)) {
+    if (a.experts > 1 || A.rows <= 16) few<T, 1, 1>(a, 4, st);
+    else if (A.rows <= 32) few<T, 2, 1>(a, 4, st);
+    else few<T, 2, 2>(a, 4, st);
+    return (int)hipGetLastError();
+  }
   a.ntiles = div_up(a.out, tile);
   // at most: experts may each end inside a tile
   const int64_t tiles = ((A.rows + tile - 1) / tile + a.experts - 1) * a.ntiles * a.splits;

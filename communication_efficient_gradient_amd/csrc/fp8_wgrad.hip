@@ -3,6 +3,8 @@
 // and its exactness: wgrad_tile.hpp):
 //   dw[e, o, c] <- beta dw[e, o, c] + sum_{t of e} dy[t, o] x^[t, c]
 //   db[e, o]    <- beta db[e, o]    + sum_{t of e} dy[t, o]
+#include <cmath>
+
 #include "fp8.hpp"
 #include "wgrad_tile.hpp"
 
@@ -18,83 +20,221 @@ struct Fp8Form {
 struct ExpertArgs {
   int experts;
   const int64_t* offsets;
+  int most;       // steps of 64 tokens that one workgroup takes
+  int share;      // tiles of an XCD of each unit; 0: tiles go round the XCDs
+  int64_t parts;  // that the workspace holds: enough for ascending tables
 };
 
-// As k_act_wgrad; the tokens of each expert are split by themselves.
+// A unit is what the tiles' workgroups take of the sum: an expert's tokens, or
+// a part of them where they are more than `most` steps.  Loads of experts
+// differ, so units are taken by length, those over half of `most` first, then
+// those over a quarter, then the rest, and no expert keeps a few workgroups
+// busy when the others are done.  (16384 tokens over 8 experts x 2048 x 2048: XXX
+// us; by expert, in the table's order, 309.)
+struct Unit {
+  int expert, split, splits;
+  int part;       // the first of the expert's parts in the workspace
+};
+
+// Each lane looks at a run of experts; the tokens' table is small and the same
+// for all waves.  `u`: the unit's number, or the split expert's (JOIN).
+template <bool JOIN>
+__device__ __forceinline__ bool find_unit(const ExpertArgs& x, int64_t rows, int u, Unit* r) {
+  const int lane = (int)threadIdx.x & 63, each = (x.experts + 63) / 64;
+  const int lo = min(lane * each, x.experts), hi = min(lo + each, x.experts);
+  auto splits_of = [&](int e, int* kind) {
+    const Tokens t = tokens_of(x.offsets, e, rows);
+    const int steps = (int)((t.hi - t.lo + 63) / 64);
+    const int s = max(1, (steps + x.most - 1) / x.most);
+    const int len = (steps + s - 1) / s;
+    *kind = JOIN ? (s > 1 ? 0 : 1) : 2 * len > x.most ? 0 : 4 * len > x.most ? 1 : 2;
+    return s;
+  };
+  int count[3] = {}, parts = 0;     // of this lane's experts
+  for (int e = lo; e < hi; ++e) {
+    int kind;
+    const int s = splits_of(e, &kind);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) count[k] += kind == k ? (JOIN ? 1 : s) : 0;
+    parts += s > 1 ? s : 0;
+  }
+  auto up_to = [&](int v) {         // of the lanes up to this one
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int w = __shfl_up(v, d);
+      if (lane >= d) v += w;
+    }
+    return v;
+  };
+  const int part0 = up_to(parts) - parts;
+  int kind = -1, first = 0, base = 0;   // the unit's kind, and this lane's first of it
+#pragma unroll
+  for (int k = 0; k < (JOIN ? 1 : 3); ++k) {
+    const int end = up_to(count[k]), total = __builtin_amdgcn_readlane(end, 63);
+    if (kind < 0 && u < base + total) {
+      kind = k;
+      first = base + end - count[k];
+    }
+    base += total;
+  }
+  if (kind < 0) return false;
+  const int mine = kind == 0 ? count[0] : kind == 1 ? count[1] : count[2];
+  const uint64_t found = __ballot(u >= first && u < first + mine);
+  Unit f = {0, 0, 1, part0};
+  if (u >= first && u < first + mine) {
+    int left = u - first;
+    for (int e = lo; e < hi; ++e) {
+      int k;
+      const int s = splits_of(e, &k), n = JOIN ? 1 : s;
+      f.expert = e;
+      f.splits = s;
+      f.split = left;
+      if (k == kind && left < n) break;
+      if (k == kind) left -= n;
+      f.part += s > 1 ? s : 0;
+    }
+  }
+  const int at = (int)__builtin_ctzll(found);
+  r->expert = __builtin_amdgcn_readlane(f.expert, at);
+  r->split = __builtin_amdgcn_readlane(f.split, at);
+  r->splits = __builtin_amdgcn_readlane(f.splits, at);
+  r->part = __builtin_amdgcn_readlane(f.part, at);
+  return true;
+}
+
+// As k_act_wgrad, a tile of a unit.
 template <typename T, bool COPY, int BO, int BC, int WO, int WC, int BK>
 __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_fp8_wgrad(WgradArgs a,
                                                                             ExpertArgs x) {
   __shared__ __attribute__((aligned(16))) char lds[wgrad_lds<T, BO, BC, BK>];
-  Tile tile;
-  if (!TileWalk(a.otiles, a.ctiles, a.splits * x.experts).take(&tile)) return;
-  const int e = tile.split / a.splits, split = tile.split - e * a.splits;
-  const Tokens r = tokens_of(x.offsets, e, a.rows);
-  const int64_t per = (r.hi - r.lo + (int64_t)64 * a.splits - 1) / ((int64_t)64 * a.splits) * 64;
-  const int64_t t0 = min(r.lo + split * per, r.hi), t1 = min(t0 + per, r.hi);
-  const bool w_part = a.splits > 1, b_part = a.splits * a.turns > 1;
-  const int64_t weight = (int64_t)a.out * a.cols;
-  float* dw = (w_part ? a.ws_w + split * quads(weight * x.experts) : a.dw) + e * weight;
-  float* db = a.db;
-  if (db) {
-    if (b_part)
-      db = a.ws_b + ((int64_t)split * a.turns + tile.j) * quads((int64_t)a.out * x.experts);
-    db += (int64_t)e * a.out;
+  const int tiles = a.otiles * a.ctiles;
+  int u, t;
+  if (x.share) {
+    const int q = (int)blockIdx.x / 8;
+    u = q / x.share;
+    t = (int)blockIdx.x % 8 * x.share + q - u * x.share;
+    if (t >= tiles) return;
+  } else {
+    u = (int)blockIdx.x / tiles;
+    t = (int)blockIdx.x - u * tiles;
   }
+  Unit unit;
+  if (!find_unit<false>(x, a.rows, u, &unit)) return;
+  const int i8 = t / (8 * a.ctiles) * 8, h = min(8, a.otiles - i8), in = t - i8 * a.ctiles;
+  const int ot = i8 + in % h, ct = in / h;
+  const Tokens r = tokens_of(x.offsets, unit.expert, a.rows);
+  const int64_t per = ((r.hi - r.lo + 63) / 64 + unit.splits - 1) / unit.splits * 64;
+  const int64_t t0 = min(r.lo + unit.split * per, r.hi), t1 = min(t0 + per, r.hi);
+  const bool part = unit.splits > 1;
+  const int64_t weight = (int64_t)a.out * a.cols, at = unit.part + unit.split;
+  if (part && at >= x.parts) return;
+  float* dw = part ? a.ws_w + at * quads(weight) : a.dw + unit.expert * weight;
+  float* db = a.db;
+  if (db) db = part ? a.ws_b + at * quads(a.out) : db + (int64_t)unit.expert * a.out;
   // a chunk of dy runs out of its row only where that stays before the
   // expert's end too
   a.free_rows = min(a.free_rows, r.hi);
-  wgrad_tile<T, Fp8Form, COPY, BO, BC, WO, WC, BK>(a, lds, tile.i, tile.j, t0, t1, r.hi, dw,
-                                                   w_part, db, b_part);
+  wgrad_tile<T, Fp8Form, COPY, BO, BC, WO, WC, BK>(a, lds, ot, ct, t0, t1, r.hi, dw, part, db,
+                                                   part);
+}
+
+// Adds the parts of the experts that have some, in order; blockIdx.y counts
+// those experts.
+__global__ __launch_bounds__(256) void k_fp8_wgrad_join(WgradArgs a, ExpertArgs x) {
+  Unit unit;
+  if (!find_unit<true>(x, a.rows, (int)blockIdx.y, &unit)) return;
+  if (unit.part + unit.splits > x.parts) return;
+  const int64_t n = (int64_t)a.out * a.cols;
+  const int64_t qw = quads(n) / 4, total = qw + (a.db ? quads(a.out) / 4 : 0);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const bool w = i < qw;
+    const int64_t e = (w ? i : i - qw) * 4, len = w ? n : a.out, stride = quads(len);
+    const float* q = (w ? a.ws_w : a.ws_b) + unit.part * stride + e;
+    f32x4 s = *(const f32x4*)q;
+    int k = 1;
+    for (; k + 8 <= unit.splits; k += 8) {
+      f32x4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = *(const f32x4*)(q + (k + j) * stride);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    for (; k < unit.splits; ++k) s += *(const f32x4*)(q + k * stride);
+    float* o = (w ? a.dw : a.db) + unit.expert * len + e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (e + j < len) o[j] = a.beta == 0.f ? s[j] : fmaf(a.beta, o[j], s[j]);
+  }
 }
 
 struct Plan {
-  int tile, splits, otiles, ctiles, turns;
+  int tile, otiles, ctiles;
+  int most;                   // steps of a unit
+  int64_t units, parts, split_experts;   // at most
 };
 
+// Tile and length of the units by an estimate of the time in microseconds: the
+// longest of what the busiest CU and one workgroup of the largest unit take, a
+// step of 64 tokens each, what a tile costs besides, and the parts' way through
+// memory and back.  How the tokens are spread is not known here: the largest of
+// several experts is taken to have three times its share, and a CU 1.3 times.
 Plan plan_wgrad(const ActDims& A, int64_t out, int experts) {
-  // as if the tokens were spread evenly over the experts
-  const int64_t each = (A.rows + experts - 1) / experts;
-  const int64_t steps = each > 0 ? (each + 63) / 64 : 1;
+  // steps of all experts together, at most: each may end inside one
+  const int64_t rows = A.rows > 0 ? A.rows : 1;
+  const int64_t some = experts < rows ? experts : rows;
+  const int64_t steps = rows / 64 + some;
+  const double largest = experts == 1 || 3 * steps > some * steps
+                             ? (double)steps : 3. * (double)steps / (double)some;
   const double big_step = A.dtype == GQ_F32 ? 5.0 : 1.9;
   const double small_step = A.dtype == GQ_F32 ? 3.4 : 1.45;
   Plan best = {};
   double least = 1e30;
   for (int tile = 128; tile <= 256; tile *= 2) {
     const int64_t ot = (out + tile - 1) / tile, ct = (A.cols + tile - 1) / tile;
-    for (int64_t s = 1; s <= 32 && (s == 1 || s * 2 <= steps); ++s) {
-      const int64_t per = (steps + s - 1) / s;
-      const int64_t groups = ot * ct * s * experts, slots = tile == 256 ? kCus : 2 * kCus;
+    const int64_t slots = tile == 256 ? kCus : 2 * kCus;
+    for (int q = 2; q <= 64; ++q) {
+      const int64_t most = (2 * steps + q - 1) / q;
+      if (q > 2 && most < 4) break;
+      const double parts = largest > (double)most ? std::ceil(largest / (double)most) : 0.;
+      const double groups = (double)(ot * ct) * ((double)some + parts);
       double step = tile == 256 ? big_step : small_step;
       if (tile == 128 && groups <= kCus) step *= 0.7;  // alone on its CU
-      double t = (double)((groups + slots - 1) / slots) *
-                 ((double)per * step + (tile == 256 ? 8.0 : 5.0));
-      if (s > 1) t += 4.0 + 8.0 * (double)(s * out * experts) * (double)A.cols / 6.5e6;
+      const double load =
+          (experts == 1 ? 1.0 : 1.3) * (double)(steps * ot * ct) / (double)slots;
+      const double unit = largest < (double)most ? largest : (double)most;
+      double t = (load > unit ? load : unit) * step +
+                 std::ceil(groups / (double)slots) * (tile == 256 ? 8.0 : 5.0);
+      if (parts > 0) t += 8.0 + 8.0 * parts * (double)out * (double)A.cols / 6.5e6;
       if (t < least) {
         least = t;
-        best = {tile, (int)s, (int)ot, (int)ct, (int)ct};
+        best = {tile, (int)ot, (int)ct, (int)most, 0, 0, 0};
       }
     }
   }
-  if (best.splits == 1 && steps <= 32) best.turns = 1;
+  // an expert of n > most steps has ceil(n / most) <= 2 n / (most + 1) parts;
+  // all steps of those experts together are `steps` at most
+  const int64_t all = steps / (best.most + 1);
+  best.split_experts = all < experts ? all : experts;
+  best.parts = best.split_experts > 0 ? steps / best.most + best.split_experts : 0;
+  best.units = experts + best.parts;
   return best;
 }
 
 // BIG, SMALL: tokens of a step for 256- and 128-tiles.
 template <typename T, bool COPY, int BIG, int SMALL>
-void wgrad_t(const WgradArgs& a, const ExpertArgs& x, int tile, hipStream_t st) {
-  const unsigned g = (unsigned)(a.otiles * a.ctiles * a.splits * x.experts);
-  if (tile == 256) k_fp8_wgrad<T, COPY, 256, 256, 128, 64, BIG><<<g, 512, 0, st>>>(a, x);
-  else k_fp8_wgrad<T, COPY, 128, 128, 64, 32, SMALL><<<g, 512, 0, st>>>(a, x);
+void wgrad_t(const WgradArgs& a, const ExpertArgs& x, const Plan& p, hipStream_t st) {
+  const int64_t g = x.share ? p.units * 8 * x.share : p.units * p.otiles * p.ctiles;
+  if (p.tile == 256)
+    k_fp8_wgrad<T, COPY, 256, 256, 128, 64, BIG><<<(unsigned)g, 512, 0, st>>>(a, x);
+  else k_fp8_wgrad<T, COPY, 128, 128, 64, 32, SMALL><<<(unsigned)g, 512, 0, st>>>(a, x);
 }
 
 }  // namespace
 
 int64_t fp8_wgrad_workspace(const ActDims& A, int64_t out, int experts) {
   const Plan p = plan_wgrad(A, out, experts);
-  const int64_t w = p.splits > 1 ? p.splits * quads(out * A.cols * experts) : 0;
-  const int64_t b =
-      p.splits * p.turns > 1 ? (int64_t)p.splits * p.turns * quads(out * experts) : 0;
-  return 4 * (w + b);
+  return 4 * p.parts * (quads(out * A.cols) + quads(out));
 }
 
 int launch_fp8_wgrad(const ActDims& A, int64_t out, int experts, const int64_t* offsets,
@@ -102,26 +242,27 @@ int launch_fp8_wgrad(const ActDims& A, int64_t out, int experts, const int64_t* 
                      float beta, float* dw, float* db, void* ws, hipStream_t st) {
   const Plan p = plan_wgrad(A, out, experts);
   float* w = (float*)ws;
-  const int64_t wn = p.splits > 1 ? p.splits * quads(out * A.cols * experts) : 0;
-  WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, 7,
-                 dy,     lddy,     rows_with_room(A.rows, lddy, 7),
-                 (const int8_t*)codes, steps, beta, dw, db,
-                 w,      w + wn,   p.splits, p.otiles, p.ctiles, p.turns, 0,
-                 out * A.cols * experts, out * experts};
-  const ExpertArgs x = {experts, offsets};
+  const WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, 7,
+                       dy,     lddy,     rows_with_room(A.rows, lddy, 7),
+                       (const int8_t*)codes, steps, beta, dw, db,
+                       w,      w + p.parts * quads(out * A.cols), 1, p.otiles, p.ctiles,
+                       1,      0,        0,        0};
+  const int tiles = p.otiles * p.ctiles;
+  const ExpertArgs x = {experts, offsets, p.most, tiles >= 32 ? div_up(tiles, 8) : 0,
+                        p.parts};
   // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
   const bool copy = A.dtype != GQ_F32 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
                     lddy < (1 << 23) && out % 8 == 0;
-  if (A.dtype == GQ_F32) wgrad_t<float, false, 32, 32>(a, x, p.tile, st);
-  else if (A.dtype == GQ_F16 && copy) wgrad_t<_Float16, true, 64, 64>(a, x, p.tile, st);
-  else if (A.dtype == GQ_F16) wgrad_t<_Float16, false, 32, 64>(a, x, p.tile, st);
-  else if (copy) wgrad_t<__bf16, true, 64, 64>(a, x, p.tile, st);
-  else wgrad_t<__bf16, false, 32, 64>(a, x, p.tile, st);
+  if (A.dtype == GQ_F32) wgrad_t<float, false, 32, 32>(a, x, p, st);
+  else if (A.dtype == GQ_F16 && copy) wgrad_t<_Float16, true, 64, 64>(a, x, p, st);
+  else if (A.dtype == GQ_F16) wgrad_t<_Float16, false, 32, 64>(a, x, p, st);
+  else if (copy) wgrad_t<__bf16, true, 64, 64>(a, x, p, st);
+  else wgrad_t<__bf16, false, 32, 64>(a, x, p, st);
   int rc = (int)hipGetLastError();
-  if (rc == 0 && (p.splits > 1 || (db && p.splits * p.turns > 1))) {
-    const int64_t n = (p.splits > 1 ? quads(out * A.cols * experts) : 0) + quads(out * experts);
-    const int64_t b = (n / 4 + 255) / 256;
-    k_act_wgrad_join<<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(a);
+  if (rc == 0 && p.parts > 0) {
+    const int64_t b = (quads(out * A.cols) / 4 + quads(out) / 4 + 255) / 256;
+    const dim3 g((unsigned)(b < 4096 ? b : 4096), (unsigned)p.split_experts);
+    k_fp8_wgrad_join<<<g, 256, 0, st>>>(a, x);
     rc = (int)hipGetLastError();
   }
   return rc;

@@ -16,6 +16,7 @@ namespace {
 
 constexpr int64_t kMaxValues = int64_t(1) << 38;
 constexpr int64_t kMaxWgradTiles = int64_t(1) << 22;  // of 128 x 128 results
+constexpr int64_t kMaxWgradRows = int64_t(1) << 34;
 
 // The form has a step per 128 columns.
 int check_fp8(const gq_act* act, gq::ActDims* A) {
@@ -49,6 +50,7 @@ int check_fp8_linear(const gq::ActDims& A, int64_t out, int32_t experts) {
 int check_fp8_wgrad(const gq::ActDims& A, int64_t out, int32_t experts) {
   const int rc = check_experts(A, out, experts);
   if (rc) return rc;
+  if (A.rows > kMaxWgradRows) return GQ_EUNSUPPORTED;
   return blocks_of(out) * blocks_of(A.cols) > kMaxWgradTiles / experts ? GQ_EUNSUPPORTED : GQ_OK;
 }
 

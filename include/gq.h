@@ -517,7 +517,7 @@ int gq_block_linear(const gq_act* act, int64_t out, int32_t experts,
  * codes, steps: the form of the layer's input.  dweight fp32 [experts][out]
  * [cols], dbias fp32 [experts][out] or NULL: slices of the flat gradient that
  * gq_quantize takes.  An expert without rows gets beta times what was there.
- * GQ_EUNSUPPORTED for more than 2^22 tiles of 128 x 128 results. */
+ * GQ_EUNSUPPORTED for more than 2^22 tiles of 128 x 128 results or 2^34 rows. */
 int gq_block_wgrad_workspace(const gq_act* act, int64_t out, int32_t experts,
                            int64_t* bytes);
 int gq_block_wgrad(const gq_act* act, int64_t out, int32_t experts,
