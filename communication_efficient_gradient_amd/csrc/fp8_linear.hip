@@ -211,26 +211,27 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   // steps of a tile's rows and of its (one or two) blocks of outputs; as many
   // slots as k-tiles, since each may be the first of another tile
   constexpr int BLOCKS = (BN + kFp8Block - 1) / kFp8Block, SLOT = (BM + 2) * 16;
-  static_assert(BM / 64 < WAVES && BLOCKS <= 2, "a wave for the weight's steps");
+  static_assert(BM / 64 < WAVES - 1 && BLOCKS <= 2, "waves for the weight's steps and the bias");
   // One array: with several the compiler tells them apart, and waits for all
   // copies before it reads from one that they may go to.
-  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * (BUF + SLOT) + sizeof(Experts)];
-  constexpr int STEPS = NS * BUF;
-  Experts& experts = *reinterpret_cast<Experts*>(&lds[NS * (BUF + SLOT)]);
+  constexpr int STEPS = NS * BUF, BIAS = STEPS + NS * SLOT, TABLE = BIAS + NS * BN * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[TABLE + sizeof(Experts)];
+  Experts& experts = *reinterpret_cast<Experts*>(&lds[TABLE]);
   const int lane = (int)threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
   read_experts<BM>(a, experts);
 
   // copies: a wave instruction fills RPI rows of codes; every fourth k-tile one
-  // more brings the steps of 64 rows, or of the weight (the waves past those).
-  // Rows past the end lie behind the buffers' ranges and read as zeros.
+  // more brings the steps of 64 rows, or of the weight (the wave past those),
+  // and every tile's first the bias (the last wave).  Rows past the end lie
+  // behind the buffers' ranges and read as zeros.
   constexpr int CM = BM / RPI / WAVES, CN = BN / RPI / WAVES;
   const int cl = lane % CH, rl = lane / CH;
   const bool row_steps = wave < BM / 64;
   const int step_at = (row_steps ? wave * 64 + lane : lane) * a.groups * 4;
   const int step_to = row_steps ? wave * 1024 : BM * 16;
-  BufferRange bm, bn, bs;
+  BufferRange bm, bn, bs;         // bs: of the steps, or the bias
   auto ranges_of = [&](const ExpertTile& t) {
     const int n = t.j * BN, rows = min(t.end - t.row, BM);
     // of this tile's rows only: shorter than kPastEnd whatever the matrix
@@ -238,7 +239,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
     bn = range_of(a.w_codes + ((int64_t)t.expert * a.out + n) * a.pitch,
                   (int64_t)min(a.out - n, BN) * a.pitch);
     const int blocks = div_up(a.out, kFp8Block), block = n / kFp8Block;
-    bs = row_steps
+    bs = wave == WAVES - 1
+             ? range_of(a.bias + (int64_t)t.expert * a.out + n,
+                        a.bias ? (int64_t)min(a.out - n, BN) * 4 : 0)
+         : row_steps
              ? range_of(a.steps + (int64_t)t.row * a.groups, (int64_t)rows * a.groups * 4)
              : range_of(a.w_steps + ((int64_t)t.expert * blocks + block) * a.groups,
                         (int64_t)min(blocks - block, BLOCKS) * a.groups * 4);
@@ -248,9 +252,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   ExpertWalk copies(experts, a.experts, a.ntiles, a.splits);
   ExpertTile ctile;
   bool copying = copies.take<BM>(&ctile);
-  int ck = 0, cend = 0, cat = 0, csteps = 0, csat = 0;
+  int ck = 0, cend = 0, cat = 0, csteps = 0, csat = 0, cbias = 0;
+  bool cfirst = true;
   auto enter = [&] {
     ranges_of(ctile);
+    cfirst = true;
     csteps = ck = ctile.split * a.per;
     cend = min(ck + a.per, k_tiles);
   };
@@ -275,6 +281,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       // what lies past a row's last step is not used
       if (row_steps || (wave == BM / 64 && lane < BLOCKS))
         copy16_to_lds(bs, step_at, ck * 4, (LdsPtr)&lds[STEPS + csat + step_to]);
+      if (wave == WAVES - 1 && cfirst) {
+        if (lane < BN / 4) copy16_to_lds(bs, lane * 16, 0, (LdsPtr)&lds[BIAS + cbias]);
+        cbias = cbias + BN * 4 == NS * BN * 4 ? 0 : cbias + BN * 4;
+        cfirst = false;
+      }
       csteps += 4;
       csat = csat + SLOT == NS * SLOT ? 0 : csat + SLOT;
     }
@@ -347,7 +358,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
 #pragma unroll
   for (int i = 0; i < NS; ++i) copy_next();
   meet(std::integral_constant<int, NS - 1>{}, !copying);
-  int at = 0;
+  int at = 0, bias = 0;           // places of the k-tile and of the tile's bias
   read_steps(0);
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
@@ -412,8 +423,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       static_assert(TOK % 32 == 0 && WM % TOK == 0, "");
       uint8_t* mine = lds + was + wave * MINE;
       const int lo = lane / 32 * 4;
-      const bool whole = n0 + BN <= a.out;
-      const float* bias = a.bias ? a.bias + (int64_t)tile.expert * a.out : nullptr;
 #pragma unroll
       for (int j0 = 0; j0 < MT; j0 += TOK / 32) {
 #pragma unroll
@@ -421,13 +430,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int n = i * 32 + q * 8 + lo;
-            float b[4] = {0.f, 0.f, 0.f, 0.f};
-            if (bias && whole) {
-              __builtin_memcpy(b, bias + n0 + wn + n, 16);
-            } else if (bias) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) b[r] = bias[min(n0 + wn + n + r, a.out - 1)];
-            }
+            const f32x4 b = *reinterpret_cast<const f32x4*>(&lds[BIAS + bias + (wn + n) * 4]);
 #pragma unroll
             for (int jj = 0; jj < TOK / 32; ++jj) {
               const int row = jj * 32 + fr;
@@ -467,6 +470,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       }
     }
     if (!walk.take<BM>(&tile)) return;
+    bias = bias + BN * 4 == NS * BN * 4 ? 0 : bias + BN * 4;
     // all waves are done with the place of the results
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -500,11 +504,11 @@ __global__ __launch_bounds__(256) void k_fp8_linear_join(LinearArgs a) {
   }
 }
 
-// Few tokens.  A workgroup takes 16 * MT tokens of an expert by 16 * NT outputs
-// (16 * MT more behind them, if there are); its eight waves take turns of four
-// k-tiles along the sum and add up in LDS.  Operands come straight from memory
-// and L2 in the products' layout, 32 codes of one row per lane, 16 rows by 128
-// codes per instruction: nothing waits for a barrier until the sums are joined.
+// Few tokens.  A workgroup takes 16 * MT tokens of an expert by 16 * NT outputs;
+// its eight waves take turns of four k-tiles along the sum and add up in LDS.
+// Operands come straight from memory and L2 in the products' layout, 32 codes of
+// one row per lane, 16 rows by 128 codes per instruction: nothing waits for a
+// barrier until the sums are joined.
 constexpr int kFewWaves = 8;
 
 template <typename T, int MT, int NT>
@@ -525,104 +529,118 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_fp8_linear_few(LinearArgs a)
                (int64_t)a.groups * 4);
   const float* bias = a.bias ? a.bias + (int64_t)expert * a.out : nullptr;
   const int row = lane % 16 * a.pitch, col = lane / 16 * 32;
-  for (int64_t m0 = t.lo + (int64_t)blockIdx.z * (16 * MT); m0 < t.hi;
-       m0 += (int64_t)gridDim.z * (16 * MT)) {
-    const int64_t rows = min(t.hi - m0, (int64_t)(16 * MT));
-    const BufferRange x = range_of(a.codes + m0 * a.pitch, rows * a.pitch);
-    const BufferRange sx = range_of(a.steps + m0 * a.groups, rows * a.groups * 4);
-    f32x4 acc[NT][MT];
+  const int64_t m0 = t.lo + (int64_t)blockIdx.z * (16 * MT);
+  if (m0 >= t.hi) return;
+  const int64_t rows = min(t.hi - m0, (int64_t)(16 * MT));
+  const BufferRange x = range_of(a.codes + m0 * a.pitch, rows * a.pitch);
+  const BufferRange sx = range_of(a.steps + m0 * a.groups, rows * a.groups * 4);
+  f32x4 acc[NT][MT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k = wave * U; k < a.groups; k += kFewWaves * U) {
-      i32x8 fw[U][NT], fx[U][MT];
-      u32x4 ew, ex[MT];
-      auto load = [&](const BufferRange& r, int c, int at) {
-        // past the pitch lies the next row: those chunks are zeros
-        const i32x4 lo = __builtin_bit_cast(
-            i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, c < a.pitch ? at + c : kPastEnd, 0, 0));
-        const i32x4 hi = __builtin_bit_cast(
-            i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       r, c + 16 < a.pitch ? at + c + 16 : kPastEnd, 0, 0));
-        return join16(lo, hi);
-      };
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = (k + u) * 128 + col;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) fw[u][j] = load(w, c, row + j * 16 * a.pitch);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) fx[u][i] = load(x, c, row + i * 16 * a.pitch);
-      }
-      ew = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(sw, k * 4, 0, 0));
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        ex[i] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       sx, ((lane % 16 + i * 16) * a.groups + k) * 4, 0, 0));
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (k + u >= a.groups) break;   // there lie other rows' steps
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            acc[j][i] = product<EXACT>(fw[u][j], fx[u][i], acc[j][i], ew[u], ex[i][u]);
-      }
-    }
-    // a lane holds four consecutive outputs of token lane % 16; kept as
-    // [token][output], 16 * NT outputs to a token
-    auto at = [&](int j, int i) {
-      return (i * 16 + lane % 16) * (16 * NT) + j * 16 + lane / 16 * 4;
+    for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k = wave * U; k < a.groups; k += kFewWaves * U) {
+    i32x8 fw[U][NT], fx[U][MT];
+    u32x4 ew, ex[MT];
+    auto load = [&](const BufferRange& r, int c, int at) {
+      // past the pitch lies the next row: those chunks are zeros
+      const i32x4 lo = __builtin_bit_cast(
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, c < a.pitch ? at + c : kPastEnd, 0, 0));
+      const i32x4 hi = __builtin_bit_cast(
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                     r, c + 16 < a.pitch ? at + c + 16 : kPastEnd, 0, 0));
+      return join16(lo, hi);
     };
-    if (wave >= HALF) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = (k + u) * 128 + col;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fw[u][j] = load(w, c, row + j * 16 * a.pitch);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[u][i] = load(x, c, row + i * 16 * a.pitch);
+    }
+    ew = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(sw, k * 4, 0, 0));
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      ex[i] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                     sx, ((lane % 16 + i * 16) * a.groups + k) * 4, 0, 0));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k + u >= a.groups) break;   // there lie other rows' steps
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          *reinterpret_cast<f32x4*>(&sums[wave - HALF][at(j, i)]) = acc[j][i];
+          acc[j][i] = product<EXACT>(fw[u][j], fx[u][i], acc[j][i], ew[u], ex[i][u]);
     }
-    __syncthreads();
-    if (wave < HALF) {
+  }
+  // a lane holds four consecutive outputs of token lane % 16; kept as
+  // [token][output], 16 * NT outputs to a token
+  auto at = [&](int j, int i) {
+    return (i * 16 + lane % 16) * (16 * NT) + j * 16 + lane / 16 * 4;
+  };
+  if (wave >= HALF) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          f32x4* p = reinterpret_cast<f32x4*>(&sums[wave][at(j, i)]);
-          *p += acc[j][i];
-        }
-    }
-    __syncthreads();
-    for (int e = (int)threadIdx.x * 4; e < E; e += kFewWaves * 64 * 4) {
-      const int64_t m = m0 + e / (16 * NT);
-      const int n = n0 + e % (16 * NT);
-      if (m >= t.hi || n >= a.out) continue;
-      f32x4 s = *reinterpret_cast<const f32x4*>(&sums[0][e]);
+      for (int i = 0; i < MT; ++i)
+        *reinterpret_cast<f32x4*>(&sums[wave - HALF][at(j, i)]) = acc[j][i];
+  }
+  __syncthreads();
+  if (wave < HALF) {
 #pragma unroll
-      for (int v = 1; v < HALF; ++v) s += *reinterpret_cast<const f32x4*>(&sums[v][e]);
-      T o[4];
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = (T)(s[r] + (bias ? bias[min(n + r, a.out - 1)] : 0.f));
-      T* y = (T*)a.y + m * a.ldy + n;
-      if (n + 4 <= a.out) {
-        __builtin_memcpy(y, o, sizeof(o));
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (n + r < a.out) y[r] = o[r];
+      for (int i = 0; i < MT; ++i) {
+        f32x4* p = reinterpret_cast<f32x4*>(&sums[wave][at(j, i)]);
+        *p += acc[j][i];
       }
+  }
+  __syncthreads();
+  for (int e = (int)threadIdx.x * 4; e < E; e += kFewWaves * 64 * 4) {
+    const int64_t m = m0 + e / (16 * NT);
+    const int n = n0 + e % (16 * NT);
+    if (m >= t.hi || n >= a.out) continue;
+    f32x4 s = *reinterpret_cast<const f32x4*>(&sums[0][e]);
+#pragma unroll
+    for (int v = 1; v < HALF; ++v) s += *reinterpret_cast<const f32x4*>(&sums[v][e]);
+    T o[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = (T)(s[r] + (bias ? bias[min(n + r, a.out - 1)] : 0.f));
+    T* y = (T*)a.y + m * a.ldy + n;
+    if (n + 4 <= a.out) {
+      __builtin_memcpy(y, o, sizeof(o));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < a.out) y[r] = o[r];
     }
-    __syncthreads();   // the sums are read
   }
 }
 
-bool few_tokens(const ActDims& A, int64_t out, int experts) { return A.rows <= 64; }
+// Which of the two: each workgroup above reads the codes of its tokens (up to
+// 32) from L2 for 16 or 32 outputs, the tiled kernel once for 64.  That is
+// little beside the weight up to 4 tokens; from there on what one CU reads so
+// decides, which is compared below.  Measured (us here / there, bf16, tokens x
+// out x cols; what is compared behind it):
+//    1 x 16384 x 8192 22.5 / 26.6          4 x 4096 x 4096  6.7 / 15.3
+//   64 x 4096 x 4096 10.8 / 15.6 (32)     16 x 8192 x 8192 17.9 / 17.6 (32)
+//   17 x 8192 x 8192 20.0 / 18.0 (34)      8 x 20000 x 8192 32.9 / 31.4 (40)
+//   12 x 16384 x 8192 29.9 / 26.7 (48)    32 x 4608 x 8192 25.4 / 15.6 (64)
+// Several experts: 32 tokens over 16 x 1024 x 2048 7.5 / 11.1, 64 over 8 x 2048 x
+// 2048 9.8 / 10.8, 64 over 64 x 1024 x 1024 17.1 / 18.0, 128 over 32 x 2048 x
+// 2048 28.1 / 25.1.
+bool few_tokens(const ActDims& A, int64_t out, int experts) {
+  if (A.rows <= 4 || A.rows > 64) return A.rows <= 4;
+  if (experts > 1) return true;
+  const int groups = A.rows <= 32 ? div_up(out, 16) : 2 * div_up(out, 32);
+  return div_up(groups, kCus) * (A.rows < 32 ? A.rows : 32) <= 32;
+}
 
 template <typename T, int MT, int NT>
-void few(const LinearArgs& a, int most, hipStream_t st) {
-  const int z = div_up(a.rows, 16 * MT);
-  const dim3 g(div_up(a.out, 16 * NT), a.experts, z < most ? z : most);
+void few(const LinearArgs& a, hipStream_t st) {
+  const dim3 g(div_up(a.out, 16 * NT), a.experts, div_up(a.rows, 16 * MT));
   k_fp8_linear_few<T, MT, NT><<<g, kFewWaves * 64, 0, st>>>(a);
 }
 
@@ -663,9 +681,9 @@ Plan plan_linear(const ActDims& A, int64_t out, int experts) {
 template <typename T>
 int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
   if (few_tokens(A, a.out, a.experts)) {
-    if (a.experts > 1 || A.rows <= 16) few<T, 1, 1>(a, 4, st);
-    else if (A.rows <= 32) few<T, 2, 1>(a, 4, st);
-    else few<T, 2, 2>(a, 4, st);
+    if (a.experts > 1 || A.rows <= 16) few<T, 1, 1>(a, st);
+    else if (A.rows <= 32) few<T, 2, 1>(a, st);
+    else few<T, 2, 2>(a, st);
     return (int)hipGetLastError();
   }
   a.ntiles = div_up(a.out, tile);
