@@ -229,14 +229,23 @@ __global__ __launch_bounds__(256) void k_grad_norm(int64_t n, const float* __res
   __shared__ double red[4];
   double s0 = 0., s1 = 0., s2 = 0., s3 = 0.;
   const int64_t quads = n / 4;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads;
-       i += (int64_t)gridDim.x * 256) {
-    const float4 w = reinterpret_cast<const float4*>(g)[i];
+  auto add = [&](const float4& w) {
     s0 = fma((double)w.x, (double)w.x, s0);
     s1 = fma((double)w.y, (double)w.y, s1);
     s2 = fma((double)w.z, (double)w.z, s2);
     s3 = fma((double)w.w, (double)w.w, s3);
+  };
+  const float4* from = reinterpret_cast<const float4*>(g);
+  const int64_t stride = (int64_t)gridDim.x * 256;
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  for (; i + 3 * stride < quads; i += 4 * stride) {   // four loads in flight
+    float4 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = from[i + u * stride];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) add(w[u]);
   }
+  for (; i < quads; i += stride) add(from[i]);
   if (blockIdx.x == 0 && (int64_t)threadIdx.x < n - quads * 4) {
     const double w = (double)g[quads * 4 + threadIdx.x];
     s0 = fma(w, w, s0);
@@ -274,8 +283,14 @@ int norm_blocks(int64_t n) {
 template <int BITS>
 int adamw_t(const AdamwArgs& a, int p16_dtype, hipStream_t st) {
   const int64_t blocks = (a.n + kStateBlock - 1) / kStateBlock;
-  int64_t per = (blocks + 8 * kCus - 1) / (8 * kCus);
-  per = (per + 3) / 4 * 4;
+  // Blocks of 256 values per workgroup of four waves: few, so that workgroups
+  // that start together do not end together (64 M values, 32 bits, 4 / 16 / 64:
+  // 329 / 346 / 361 us; 8 bits, which have more to compute and find their layer
+  // first, 4 / 8 / 16 / 64: 213 / 202 / 200 / 216 us, 3 M values 15.7 / 15.4 / 17.0 /
+  // 32), but no more workgroups than 2^22.
+  int64_t per = BITS == 32 ? 4 : 8;
+  const int64_t least = (blocks + (1 << 22) - 1) >> 22;
+  if (per < least) per = (least + 3) / 4 * 4;
   const unsigned g = (unsigned)((blocks + per - 1) / per);
   if (!a.p16) k_adamw<BITS, void><<<g, 256, 0, st>>>(a, blocks, per);
   else if (p16_dtype == GQ_BF16) k_adamw<BITS, __bf16><<<g, 256, 0, st>>>(a, blocks, per);
