@@ -22,8 +22,8 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
   float* dw = w_part ? a.ws_w + tile.split * quads((int64_t)a.out * a.cols) : a.dw;
   float* db = a.db;
   if (db && b_part) db = a.ws_b + ((int64_t)tile.split * a.turns + tile.j) * quads(a.out);
-  wgrad_tile<T, Int8Form, COPY, BO, BC, WO, WC, BK>(a, lds, tile.i, tile.j, t0, t1, a.rows, dw,
-                                                    w_part, db, b_part);
+  wgrad_tile<T, Int8Form, COPY, false, BO, BC, WO, WC, BK>(a, lds, tile.i, tile.j, t0, t1,
+                                                           a.rows, dw, w_part, db, b_part);
 }
 
 struct Plan {

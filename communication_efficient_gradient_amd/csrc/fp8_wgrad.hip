@@ -134,8 +134,8 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_fp8_wgrad(Wgr
   // a chunk of dy runs out of its row only where that stays before the
   // expert's end too
   a.free_rows = min(a.free_rows, r.hi);
-  wgrad_tile<T, Fp8Form, COPY, BO, BC, WO, WC, BK>(a, lds, ot, ct, t0, t1, r.hi, dw, part, db,
-                                                   part);
+  wgrad_tile<T, Fp8Form, COPY, COPY, BO, BC, WO, WC, BK>(a, lds, ot, ct, t0, t1, r.hi, dw, part,
+                                                         db, part);
 }
 
 // Adds the parts of the experts that have some, in order; blockIdx.y counts
@@ -242,7 +242,7 @@ int launch_fp8_wgrad(const ActDims& A, int64_t out, int experts, const int64_t* 
                      float beta, float* dw, float* db, void* ws, hipStream_t st) {
   const Plan p = plan_wgrad(A, out, experts);
   float* w = (float*)ws;
-  const WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, 7,
+  WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, 7,
                        dy,     lddy,     rows_with_room(A.rows, lddy, 7),
                        (const int8_t*)codes, steps, beta, dw, db,
                        w,      w + p.parts * quads(out * A.cols), 1, p.otiles, p.ctiles,
@@ -253,6 +253,9 @@ int launch_fp8_wgrad(const ActDims& A, int64_t out, int experts, const int64_t* 
   // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
   const bool copy = A.dtype != GQ_F32 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
                     lddy < (1 << 23) && out % 8 == 0;
+  // the bias's columns over the tiles of a row, 32 to a tile at least
+  if (copy)
+    while (a.turns * 2 <= p.ctiles && a.turns * 2 <= p.tile / 32) a.turns *= 2;
   if (A.dtype == GQ_F32) wgrad_t<float, false, 32, 32>(a, x, p, st);
   else if (A.dtype == GQ_F16 && copy) wgrad_t<_Float16, true, 64, 64>(a, x, p, st);
   else if (A.dtype == GQ_F16) wgrad_t<_Float16, false, 32, 64>(a, x, p, st);

@@ -120,12 +120,12 @@ __device__ __forceinline__ u32x4 packed(const float (&f)[8]) {
 // The sum runs over the tokens t0 .. t1 - 1; tokens from `end` on (t1 or
 // further) read as zeros.  dw, db: of the tile's weight, or its part of them
 // (db NULL: no bias; `parts`: a part, which beta does not concern).
-template <typename T, typename Form, bool COPY, int BO, int BC, int WO, int WC, int BK>
+template <typename T, typename Form, bool COPY, bool COLS, int BO, int BC, int WO, int WC, int BK>
 __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot, int ct,
                                            int64_t t0, int64_t t1, int64_t end, float* dw,
                                            bool w_part, float* db, bool b_part) {
   constexpr int P = kPlanes<T>;
-  static_assert(!COPY || P == 1, "");
+  static_assert(COPY ? P == 1 : !COLS, "");
   constexpr int WAVES = (BO / WO) * (BC / WC), TH = WAVES * 64;
   constexpr int OT = WO / 32, CT = WC / 32, KK = BK / 16;
   constexpr int ABUF = P * BK * BO * 2, BBUF = BK * BC * 2, BUF = ABUF + BBUF;
@@ -248,19 +248,30 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot
         packed<T>(f);
   };
 
-  // The bias's sums are shared out over the tiles of a row: tile ct < turns
-  // takes the steps st with st % turns == ct.
+  // The bias's sums are shared out over the tiles of a row.  Tile ct < turns
+  // takes the steps st with st % turns == ct, which gives parts, or (COLS, turns
+  // a power of two) 1 / turns of the columns: `ppt` pieces of eight of each row.
   const bool bias = db != nullptr && ct < a.turns;
+  const int ppt = COLS ? LPR / a.turns : LPR;
+  auto add_piece = [&](LdsPtr from, int t, int p) {
+    const u32x4 u = *(GQ_LDS u32x4*)(from + place<BO>(t, p / 2) + p % 2 * 16);
+    float v[8];
+    widen(__builtin_bit_cast(Raw8<std::conditional_t<sizeof(T) == 2, T, __bf16>>, u), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bsum[j] += v[j];
+  };
   auto sum_dy = [&](LdsPtr from) {
+    if constexpr (COLS) {
+      // a thread's pieces lie in the same columns: TH is a multiple of ppt
+      for (int q = tid; q < BK * ppt; q += TH)
+        add_piece(from, q / ppt, ct * ppt + tid % ppt);
+      return;
+    }
     constexpr int N = BK * BO / 8 / TH;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int q = i * TH + tid, t = q / LPR, p = q % LPR;
-      const u32x4 u = *(GQ_LDS u32x4*)(from + place<BO>(t, p / 2) + p % 2 * 16);
-      float v[8];
-      widen(__builtin_bit_cast(Raw8<std::conditional_t<sizeof(T) == 2, T, __bf16>>, u), v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) bsum[j] += v[j];
+      const int q = i * TH + tid;
+      add_piece(from, q / LPR, q % LPR);
     }
   };
 
@@ -300,7 +311,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot
   auto step = [&](int st, LdsPtr __restrict__ now_a, LdsPtr __restrict__ now_b,
                   LdsPtr __restrict__ next_a, LdsPtr __restrict__ next_b) {
     turn = turn + 1 == a.turns ? 0 : turn + 1;
-    const bool sum = bias && turn == ct && st + 1 < steps;
+    const bool sum = !COLS && bias && turn == ct && st + 1 < steps;
     if constexpr (COPY) copy_dy(next_a);
     next_codes();
 #pragma unroll
@@ -336,6 +347,8 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot
 #pragma unroll
         for (int j = 0; j < CT; ++j)
           acc[i][j] = product<T>(fa[k & 1][i], fb[kk & 1][j], acc[i][j]);
+      // in the middle of the step: right behind the barrier nothing hides it
+      if (COLS && k == 0 && bias) sum_dy(now_a);
       // reads and decoding between products
 #pragma unroll
       for (int g = 0; g < OT * CT; ++g) {
@@ -365,7 +378,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot
       load_codes(i);
     }
     __syncthreads();
-    if (COPY && bias && ct == 0) sum_dy(a0);
+    if (COPY && !COLS && bias && ct == 0) sum_dy(a0);
     read_a(0, a0, 0);
     read_b(0, b0, 0);
   }
@@ -394,11 +407,29 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot
   }
   if (bias) {
     // threads of one piece of columns hold sums of different rows
+    const int width = ppt * 8, groups = TH / ppt;
     __syncthreads();
-    float* sh = reinterpret_cast<float*>(lds);  // [TH / LPR][BO]
+    float* sh = reinterpret_cast<float*>(lds);  // [groups][width]
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sh[tid / LPR * BO + tid % LPR * 8 + j] = bsum[j];
+    for (int j = 0; j < 8; ++j) sh[tid / ppt * width + tid % ppt * 8 + j] = bsum[j];
     __syncthreads();
+    if constexpr (COLS) {
+      // 8 groups to a thread first, then those TH / width sums
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) s += sh[(tid / width * 8 + g) * width + tid % width];
+      __syncthreads();
+      sh[tid] = s;
+      __syncthreads();
+      const int o = o0 + ct * width + tid;
+      if (tid < width && o < a.out) {
+        s = 0.f;
+        for (int g = 0; g < TH / width; ++g) s += sh[g * width + tid];
+        float* q = db + o;
+        *q = b_part || a.beta == 0.f ? s : fmaf(a.beta, *q, s);
+      }
+      return;
+    }
     for (int o = tid; o < BO && o0 + o < a.out; o += TH) {
       float s = 0.f;
 #pragma unroll
