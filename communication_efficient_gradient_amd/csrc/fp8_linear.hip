@@ -197,8 +197,7 @@ __device__ __forceinline__ f32x4 product(i32x8 a, i32x8 b, f32x4 c, uint32_t sa,
 // one chunk of sixteen rows then touch every bank once.  NS k-tiles share LDS:
 // one is multiplied while NS - 1 are on their way.  Steps come for four k-tiles
 // at once, since each row's lie in a line of their own (a fetch per k-tile
-// makes half as many requests again as the codes do: 322 us instead of XXX for
-// 8192 x 8192 x 4096 from HBM).  Workgroups stay and walk the tiles, and the copies
+// makes half as many requests again as the codes do).  Workgroups stay and walk the tiles, and the copies
 // run on into the next tile while the present one's last products run and its
 // results leave.
 template <typename T, int BM, int BN, int WM, int WN, int NS>

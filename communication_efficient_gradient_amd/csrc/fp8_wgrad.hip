@@ -29,8 +29,8 @@ struct ExpertArgs {
 // a part of them where they are more than `most` steps.  Loads of experts
 // differ, so units are taken by length, those over half of `most` first, then
 // those over a quarter, then the rest, and no expert keeps a few workgroups
-// busy when the others are done.  (16384 tokens over 8 experts x 2048 x 2048: XXX
-// us; by expert, in the table's order, 309.)
+// busy when the others are done (16384 tokens over 8 experts x 2048 x 2048 in the
+// table's order, whole: 326 us).
 struct Unit {
   int expert, split, splits;
   int part;       // the first of the expert's parts in the workspace
@@ -177,40 +177,64 @@ struct Plan {
 // Tile and length of the units by an estimate of the time in microseconds: the
 // longest of what the busiest CU and one workgroup of the largest unit take, a
 // step of 64 tokens each, what a tile costs besides, and the parts' way through
-// memory and back.  How the tokens are spread is not known here: the largest of
-// several experts is taken to have three times its share, and a CU 1.3 times.
+// memory and back.  How the tokens are spread over several experts is not known
+// here: the largest is taken to have three times its share, a CU 1.3 times.
+// Parts are only written where an expert has more than a unit, else they cost
+// the empty launch that would join them: units may end at a CU's share even if
+// none is expected to (16384 tokens over 8 x 2048 x 2048, loads as drawn for six
+// batches: 187 us with units of 86 steps, 237 with any; 2048 tokens 69 / 65 / 61
+// us with 16 / 32 / any).
 Plan plan_wgrad(const ActDims& A, int64_t out, int experts) {
   // steps of all experts together, at most: each may end inside one
   const int64_t rows = A.rows > 0 ? A.rows : 1;
   const int64_t some = experts < rows ? experts : rows;
   const int64_t steps = rows / 64 + some;
-  const double largest = experts == 1 || 3 * steps > some * steps
-                             ? (double)steps : 3. * (double)steps / (double)some;
+  auto share = [&](double times) {
+    return times < (double)some ? times * (double)steps / (double)some : (double)steps;
+  };
   const double big_step = A.dtype == GQ_F32 ? 5.0 : 1.9;
   const double small_step = A.dtype == GQ_F32 ? 3.4 : 1.45;
   Plan best = {};
   double least = 1e30;
+  auto consider = [&](int tile, int64_t ot, int64_t ct, int64_t most, double t) {
+    if (t >= least) return;
+    least = t;
+    best = {tile, (int)ot, (int)ct, (int)most, 0, 0, 0};
+  };
   for (int tile = 128; tile <= 256; tile *= 2) {
     const int64_t ot = (out + tile - 1) / tile, ct = (A.cols + tile - 1) / tile;
-    const int64_t slots = tile == 256 ? kCus : 2 * kCus;
-    for (int q = 2; q <= 64; ++q) {
-      const int64_t most = (2 * steps + q - 1) / q;
-      if (q > 2 && most < 4) break;
-      const double parts = largest > (double)most ? std::ceil(largest / (double)most) : 0.;
-      const double groups = (double)(ot * ct) * ((double)some + parts);
+    const double slots = tile == 256 ? kCus : 2 * kCus, tiles = (double)(ot * ct);
+    const double load = (double)steps * tiles / slots;
+    // of `units` units, the longest `unit` steps, and `parts` parts
+    auto time = [&](double load, double unit, double units, double parts) {
       double step = tile == 256 ? big_step : small_step;
-      if (tile == 128 && groups <= kCus) step *= 0.7;  // alone on its CU
-      const double load =
-          (experts == 1 ? 1.0 : 1.3) * (double)(steps * ot * ct) / (double)slots;
-      const double unit = largest < (double)most ? largest : (double)most;
-      double t = (load > unit ? load : unit) * step +
-                 std::ceil(groups / (double)slots) * (tile == 256 ? 8.0 : 5.0);
-      if (parts > 0) t += 8.0 + 8.0 * parts * (double)out * (double)A.cols / 6.5e6;
-      if (t < least) {
-        least = t;
-        best = {tile, (int)ot, (int)ct, (int)most, 0, 0, 0};
+      if (tile == 128 && tiles * units <= kCus) step *= 0.7;  // alone on its CU
+      const double t = (load > unit ? load : unit) * step +
+                       std::ceil(tiles * units / slots) * (tile == 256 ? 8.0 : 5.0);
+      return parts == 0. ? t : t + 8.0 + 8.0 * parts * (double)out * (double)A.cols / 6.5e6;
+    };
+    if (some == 1) {
+      for (int64_t s = 1; s <= 32 && (s == 1 || steps / s >= 4); ++s) {
+        const int64_t most = (steps + s - 1) / s;
+        consider(tile, ot, ct, most,
+                 time(load, (double)most, (double)s, s > 1 ? (double)s : 0.));
       }
+      continue;
     }
+    const double cu = 1.3 * load, large = share(3.), one = share(1.);
+    auto several = [&](int64_t most) {
+      const double m = (double)most;
+      const double parts = one > m     ? (double)some * std::ceil(one / m)
+                           : large > m ? std::ceil(large / m) : 0.;
+      const double units = one > m ? parts : (double)some + parts;
+      consider(tile, ot, ct, most,
+               time(cu, large < m ? large : m, units, parts) + (most < steps ? 4.0 : 0.));
+    };
+    for (int64_t s = 1; s <= 32 && (s == 1 || steps / s >= 4); ++s)
+      several((steps + s - 1) / s);
+    const double m = std::ceil(cu);
+    if (m > 32.)
+      consider(tile, ot, ct, (int64_t)m, 4.0 + time(cu, large < m ? large : m, (double)some, 0.));
   }
   // an expert of n > most steps has ceil(n / most) <= 2 n / (most + 1) parts;
   // all steps of those experts together are `steps` at most

@@ -407,9 +407,9 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot
   }
   if (bias) {
     // threads of one piece of columns hold sums of different rows
-    const int width = ppt * 8, groups = TH / ppt;
+    const int width = ppt * 8;
     __syncthreads();
-    float* sh = reinterpret_cast<float*>(lds);  // [groups][width]
+    float* sh = reinterpret_cast<float*>(lds);  // [TH / ppt][width]
 #pragma unroll
     for (int j = 0; j < 8; ++j) sh[tid / ppt * width + tid % ppt * 8 + j] = bsum[j];
     __syncthreads();
