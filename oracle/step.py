@@ -131,10 +131,11 @@ def wgrad(dy, x, offsets):
 
 
 # ------------------------------------------------------------- the step ----
-def philox(seed: int, step: int, n: int) -> np.ndarray:
-    """Word i mod 4 of Philox4x32-10 at the counter (i / 4, step), for i < n."""
-    low = np.uint64(0xffffffff)
-    i = np.arange(-(-n // 4), dtype=np.uint64)
+def philox(seed: int, step: int, n: int, first: int = 0) -> np.ndarray:
+    """Word i mod 4 of Philox4x32-10 at the counter (i / 4, step), for n values i
+    from `first` on."""
+    low, skip = np.uint64(0xffffffff), first % 4
+    i = np.arange(-(-(n + skip) // 4), dtype=np.uint64) + np.uint64(first // 4)
     c = [i & low, i >> np.uint64(32), np.full_like(i, step), np.zeros_like(i)]
     k = [seed & 0xffffffff, seed >> 32]
     for _ in range(10):
@@ -142,7 +143,7 @@ def philox(seed: int, step: int, n: int) -> np.ndarray:
         c = [(b >> np.uint64(32)) ^ c[1] ^ np.uint64(k[0]), b & low,
              (a >> np.uint64(32)) ^ c[3] ^ np.uint64(k[1]), a & low]
         k = [(k[0] + 0x9E3779B9) & 0xffffffff, (k[1] + 0xBB67AE85) & 0xffffffff]
-    return np.stack(c, 1).reshape(-1)[:n]
+    return np.stack(c, 1).reshape(-1)[skip:skip + n]
 
 
 def state_codes(x, r16, table, top: float):

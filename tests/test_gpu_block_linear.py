@@ -171,48 +171,86 @@ def test_tables_out_of_range_stay_in_bounds(gq):
     torch.cuda.synchronize()
 
 
-def test_steps_that_are_not_finite_stay_alone(gq):
-    rows, out, cols = 150, 300, 400
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,split", [(150, 70), (30, 9)])
+def test_steps_that_are_not_finite_stay_alone(gq, dtype, rows, split):
+    out, cols = 300, 400
     x, w, b = forms(4, rows, out, cols, 2, True)
     x[1][3, 1] = np.nan
     x[0][3, 128:256] = 0
     w[1][1, 1, 2] = np.nan
     w[0][1, 128:256, 256:384] = 0
-    off = np.array([0, 70, rows], np.int64)
-    y = run(gq, x, w, b, off, rows, out, cols, "f32").cpu().numpy()
+    off = np.array([0, split, rows], np.int64)
+    y = run(gq, x, w, b, off, rows, out, cols, dtype).double().cpu().numpy()
     want, _ = S.linear(S.unpack(*x, cols), S.unpack_weight(*w, cols), b, off)
     bad = np.isnan(want)
-    assert bad[3].all() and bad[70:, 128:256].all() and bad.sum() == out + 80 * 128
+    assert bad[3].all() and bad[split:, 128:256].all()
+    assert bad.sum() == out + (rows - split) * 128
     assert np.array_equal(np.isnan(y), bad)
-    assert np.array_equal(y[~bad], want[~bad].astype(np.float32))
+    exact = torch.as_tensor(want).float().to(TYPES[dtype]).double().numpy()
+    assert np.array_equal(y[~bad], exact[~bad])
 
 
-def test_codes_that_are_nan(gq):
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows", [20, 200])
+def test_codes_that_are_nan(gq, dtype, rows):
     """e4m3's NaN is a code like any other: its row and its outputs."""
-    rows, out, cols = 20, 140, 200
+    out, cols = 140, 200
     x, w, b = forms(5, rows, out, cols, 1, True)
     x[0][7, 150] = 0x7f
     w[0][0, 9, 3] = 0xff
-    y = run(gq, x, w, b, None, rows, out, cols, "f32").cpu().numpy()
+    y = run(gq, x, w, b, None, rows, out, cols, dtype).float().cpu().numpy()
     bad = np.zeros((rows, out), bool)
     bad[7], bad[:, 9] = True, True
     assert np.array_equal(np.isnan(y), bad)
 
 
-def test_extreme_steps(gq):
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("each", [50, 300])
+def test_extreme_steps(gq, dtype, each):
     """Every exponent that a form can have, with the other side's opposite."""
-    e = np.arange(-126, 120)
-    rows, cols = len(e), 128
-    x = np.zeros((rows, 128), np.uint8)
-    x[:, 5] = 0x38
-    w = np.zeros((1, 1, 128), np.uint8)
-    w[0, 0, 5] = 0xb9           # -1.125
-    for k in (-3, 0, 6):
-        y = run(gq, (x, np.exp2(e)[:, None].astype(np.float32)),
-                (w, np.full((1, 1, 1), 2.0 ** k, np.float32)), None, None, rows, 1, cols, "f32")
-        want = (-1.125 * np.exp2(e.astype(np.float64) + k)).astype(np.float32)
-        fine = np.abs(want) >= 2.0 ** -126      # below: may be flushed
-        assert np.array_equal(y.cpu().numpy()[fine, 0], want[fine])
+    for lo in range(-126, 120, each):
+        e = np.arange(lo, min(lo + each, 120))
+        rows, cols = len(e), 128
+        x = np.zeros((rows, 128), np.uint8)
+        x[:, 5] = 0x38
+        w = np.zeros((1, 1, 128), np.uint8)
+        w[0, 0, 5] = 0xb9           # -1.125
+        for k in (-3, 0, 6):
+            y = run(gq, (x, np.exp2(e)[:, None].astype(np.float32)),
+                    (w, np.full((1, 1, 1), 2.0 ** k, np.float32)), None, None, rows, 1, cols,
+                    dtype)
+            want = (-1.125 * np.exp2(e.astype(np.float64) + k)).astype(np.float32)
+            fine = np.abs(want) >= 2.0 ** -126      # below: may be flushed
+            assert np.array_equal(y.float().cpu().numpy()[fine, 0], want[fine])
+
+
+def behind(values, dtype, poison, rows=200):
+    """A contiguous device array with `rows` more of poison behind it."""
+    buf = torch.full((values.shape[0] + rows,) + values.shape[1:], poison, device="cuda",
+                     dtype=dtype)
+    buf[:values.shape[0]] = torch.as_tensor(values)
+    return buf[:values.shape[0]]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 17, 33, 50, 65, 130, 300])
+@pytest.mark.parametrize("out,cols", [(1, 16), (17, 100), (40, 64), (63, 1000), (131, 272)])
+def test_reads_zeros_behind_the_last_rows(gq, dtype, rows, out, cols):
+    """Codes, steps, weights and biases of other things behind the matrices."""
+    x, w, b = forms(rows, rows, out, cols, 2, True)
+    off = np.array([0, rows // 2, rows], np.int64)
+    a = gq.act(rows, cols, TYPES[dtype], 128)
+    y = torch.full((rows + 9, out), 77.0, device="cuda", dtype=TYPES[dtype])
+    nan = float("nan")
+    gq.gq_block_linear(
+        a, behind(x[0], torch.uint8, 0x7f).view(E4M3), behind(x[1], torch.float32, nan),
+        behind(w[0], torch.uint8, 0x7f).view(E4M3), behind(w[1], torch.float32, nan),
+        behind(b, torch.float32, nan), y[:rows], offsets=dev(off),
+        workspace=gq.alloc_workspace(gq.gq_block_linear_workspace(a, out, 2)))
+    want, _ = S.linear(S.unpack(*x, cols), S.unpack_weight(*w, cols), b, off)
+    assert torch.equal(y[:rows].cpu(), torch.as_tensor(want).float().to(TYPES[dtype]))
+    assert bool((y[rows:] == 77.0).all())
 
 
 def test_no_rows(gq):
