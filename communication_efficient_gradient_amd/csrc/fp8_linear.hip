@@ -22,21 +22,18 @@ namespace {
 
 typedef __attribute__((address_space(3))) uint8_t* LdsPtr;
 
-template <typename T>
-struct Word16 {
-  typedef T V __attribute__((ext_vector_type(16 / sizeof(T))));
-};
-
 // Up to 16 bytes of a row of y, of which `valid` values exist.
-template <typename T, typename V>
-__device__ __forceinline__ void store_piece(T* y, const V& w, int valid) {
+template <typename T>
+__device__ __forceinline__ void store_piece(T* y, const u32x4& w, int valid) {
   constexpr int E = 16 / (int)sizeof(T);
   if (valid >= E) {
     __builtin_memcpy(y, &w, 16);
   } else {
+    T o[E];
+    __builtin_memcpy(o, &w, 16);
 #pragma unroll
     for (int j = 0; j < E; ++j)
-      if (j < valid) y[j] = w[j];
+      if (j < valid) y[j] = o[j];
   }
 }
 
@@ -149,6 +146,35 @@ __device__ __forceinline__ i32x8 join16(i32x4 a, i32x4 b) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// Among N neighbouring lanes (2 or 4): lane a's u[k] <- lane k's u[a].
+template <int N>
+__device__ __forceinline__ void transpose_lanes(u32x4 (&u)[N]) {
+  const int lane = (int)threadIdx.x;
+#pragma unroll
+  for (int d = 1; d < N; d *= 2)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (k & d) continue;
+      const bool hi = (lane & d) != 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t x = u[k][w], y = u[k | d][w];
+        const uint32_t r = xshfl(hi ? x : y, d);
+        u[k][w] = hi ? r : x;
+        u[k | d][w] = hi ? y : r;
+      }
+    }
+}
+
+// Four consecutive results of a lane as the words of their type.
+template <typename T>
+__device__ __forceinline__ void words_of(const f32x4& v, uint32_t* w) {
+  T o[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] = (T)v[r];
+  __builtin_memcpy(w, o, sizeof(o));
+}
+
 // Eight codes times their step in bf16.
 __device__ __forceinline__ bf16x8 bf16_of(int lo, int hi, float step) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -207,13 +233,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   constexpr int WAVES = (BM / WM) * (BN / WN);
   constexpr int MT = WM / 32, NTL = WN / 32;
   constexpr int BUF = (BM + BN) * BK;
+  // results leave in pieces of 16 bytes: a lane has UNITS of each 32 tokens
+  constexpr int E = 16 / (int)sizeof(T), UNITS = WN / (2 * E), STORES = MT * UNITS;
   // steps of a tile's rows and of its (one or two) blocks of outputs; as many
-  // slots as k-tiles, since each may be the first of another tile
+  // slots as k-tiles, since each may be the first of another tile.  One slot
+  // more for the bias, which is used when the copies are NS k-tiles ahead.
   constexpr int BLOCKS = (BN + kFp8Block - 1) / kFp8Block, SLOT = (BM + 2) * 16;
   static_assert(BM / 64 < WAVES - 1 && BLOCKS <= 2, "waves for the weight's steps and the bias");
   // One array: with several the compiler tells them apart, and waits for all
   // copies before it reads from one that they may go to.
-  constexpr int STEPS = NS * BUF, BIAS = STEPS + NS * SLOT, TABLE = BIAS + NS * BN * 4;
+  constexpr int STEPS = NS * BUF, BIAS = STEPS + NS * SLOT, TABLE = BIAS + (NS + 1) * BN * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TABLE + sizeof(Experts)];
   Experts& experts = *reinterpret_cast<Experts*>(&lds[TABLE]);
   const int lane = (int)threadIdx.x & 63;
@@ -282,7 +311,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
         copy16_to_lds(bs, step_at, ck * 4, (LdsPtr)&lds[STEPS + csat + step_to]);
       if (wave == WAVES - 1 && cfirst) {
         if (lane < BN / 4) copy16_to_lds(bs, lane * 16, 0, (LdsPtr)&lds[BIAS + cbias]);
-        cbias = cbias + BN * 4 == NS * BN * 4 ? 0 : cbias + BN * 4;
+        cbias = cbias == NS * BN * 4 ? 0 : cbias + BN * 4;
         cfirst = false;
       }
       csteps += 4;
@@ -295,14 +324,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
     }
   };
   // Waits until this wave's reads are done and its copies but those of the
-  // LEFT youngest k-tiles have arrived, then for the other waves.  Copies arrive
-  // in order; anything else in flight (steps, results on their way out) only
-  // makes the wait longer.  Once there is nothing left to copy the youngest are
-  // fewer, so all are waited for.
-  auto meet = [&](auto left, bool all) {
+  // LEFT youngest k-tiles have arrived, then for the other waves.  Copies and
+  // stores are done with in order.  `stored`: behind those copies there are the
+  // STORES of a whole tile's results, which need not have left; anything else in
+  // flight (steps, other results) only makes the wait longer.  Once there is
+  // nothing left to copy the youngest are fewer, so all are waited for.
+  auto meet = [&](auto left, bool all, bool stored) {
     constexpr int LEFT = decltype(left)::value;
-    if (LEFT == 0 || all) {
+    if (all) {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    } else if (stored) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT * (CM + CN) + STORES) : "memory");
     } else {
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT * (CM + CN)) : "memory");
     }
@@ -356,8 +388,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   enter();
 #pragma unroll
   for (int i = 0; i < NS; ++i) copy_next();
-  meet(std::integral_constant<int, NS - 1>{}, !copying);
+  meet(std::integral_constant<int, NS - 1>{}, !copying, false);
   int at = 0, bias = 0;           // places of the k-tile and of the tile's bias
+  bool stored = false;
   read_steps(0);
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
@@ -374,9 +407,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    int was = at;
     for (int kt = first; kt < last; ++kt) {
-      was = at;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         if (kk == 1) {
@@ -386,10 +417,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
           for (int i = 0; i < NTL; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[i][j]));
-          // the next k-tile is in LDS and this one is read: its place is free,
-          // but for the last one's, through which the results leave first
-          meet(std::integral_constant<int, NS - 2>{}, !copying);
-          if (kt + 1 < last) copy_next();
+          // the next k-tile is in LDS and this one is read: its place is free
+          meet(std::integral_constant<int, NS - 2>{}, !copying, stored);
+          stored = false;
+          copy_next();
           at = at + BUF == NS * BUF ? 0 : at + BUF;
           next_steps(kt + 1 == last ? 0 : kt + 1 - first);
           read_steps(1);
@@ -410,45 +441,57 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       en[0] = en[1];
     }
     // A lane holds, of one token per 32 x 32 tile, four consecutive outputs in
-    // each of the tile's four quarters: eight bytes of bf16, at 32 rows of y.
-    // The wave's results therefore go through its own part of the buffer that
-    // the last k-tile left, TOK tokens at a time, and leave as whole 16-byte
-    // pieces of WN-long rows.
+    // each of the tile's four quarters, the lane 32 further the next four.  In 16
+    // bits the two first swap halves, so that each has eight consecutive outputs
+    // of every second quarter.  Then neighbouring lanes, which have neighbouring
+    // tokens, exchange their 16-byte pieces: each store writes whole lines (128
+    // bytes of a row; 64 where the wave's part is 32 outputs of 16 bits).
     if (a.splits == 1) {
-      using V = typename Word16<T>::V;  // 16 bytes of results
-      constexpr int E = 16 / (int)sizeof(T), ROW = WN / E;  // pieces per row
-      constexpr int MINE = BUF / WAVES, FIT = MINE / (WN * (int)sizeof(T));
-      constexpr int TOK = FIT < WM ? FIT : WM;
-      static_assert(TOK % 32 == 0 && WM % TOK == 0, "");
-      uint8_t* mine = lds + was + wave * MINE;
-      const int lo = lane / 32 * 4;
+      constexpr int G = UNITS < 4 ? UNITS : 4;    // lanes that exchange
+      const int half = lane / 32, nb = lane % G;
+      stored = tile.row + BM <= tile.end && n0 + BN <= a.out;
 #pragma unroll
-      for (int j0 = 0; j0 < MT; j0 += TOK / 32) {
+      for (int j = 0; j < MT; ++j) {
+        u32x4 u[UNITS / G][G];
 #pragma unroll
         for (int i = 0; i < NTL; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int n = i * 32 + q * 8 + lo;
-            const f32x4 b = *reinterpret_cast<const f32x4*>(&lds[BIAS + bias + (wn + n) * 4]);
+          for (int q = 0; q < 4; q += sizeof(T) == 2 ? 2 : 1) {
+            auto result = [&](int q) {
+              const int n = wn + i * 32 + q * 8 + half * 4;
+              const f32x4 b = *reinterpret_cast<const f32x4*>(&lds[BIAS + bias + n * 4]);
+              f32x4 v;
 #pragma unroll
-            for (int jj = 0; jj < TOK / 32; ++jj) {
-              const int row = jj * 32 + fr;
-              T o[4];
+              for (int r = 0; r < 4; ++r) v[r] = acc[i][j][q * 4 + r] + b[r];
+              return v;
+            };
+            u32x4 w;
+            if constexpr (sizeof(T) == 2) {
+              uint32_t x[2], y[2];
+              words_of<T>(result(q), x);
+              words_of<T>(result(q + 1), y);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) o[r] = (T)(acc[i][j0 + jj][q * 4 + r] + b[r]);
-              // piece p of row `row` is kept at place p ^ (row % ROW)
-              __builtin_memcpy(
-                  mine + (row * ROW + ((n / E) ^ (row % ROW))) * 16 + n % E * (int)sizeof(T),
-                  o, sizeof(o));
+              for (int r = 0; r < 2; ++r) {
+                const auto z = __builtin_amdgcn_permlane32_swap(x[r], y[r], false, false);
+                w[r] = z[0];
+                w[2 + r] = z[1];
+              }
+            } else {
+              w = __builtin_bit_cast(u32x4, result(q));
             }
+            const int k = sizeof(T) == 2 ? i * 2 + q / 2 : i * 4 + q;
+            u[k / G][k % G] = w;
           }
 #pragma unroll
-        for (int k = 0; k < TOK * ROW / 64; ++k) {
-          const int row = (k * 64 + lane) / ROW, p = lane % ROW;
-          const V w = *reinterpret_cast<const V*>(mine + (row * ROW + (p ^ (row % ROW))) * 16);
-          const int m = tile.row + wm + j0 * 32 + row;
-          const int n = n0 + wn + p * E;
-          if (m < tile.end) store_piece((T*)a.y + m * a.ldy + n, w, a.out - n);
+        for (int g = 0; g < UNITS / G; ++g) {
+          transpose_lanes(u[g]);
+          // piece nb of the group, of token k of the neighbours
+          const int n = n0 + wn + (g * G + nb) * (2 * E) + half * E;
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            const int m = tile.row + wm + j * 32 + fr - nb + k;
+            if (m < tile.end) store_piece((T*)a.y + m * a.ldy + n, u[g][k], a.out - n);
+          }
         }
       }
     } else {
@@ -469,12 +512,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       }
     }
     if (!walk.take<BM>(&tile)) return;
-    bias = bias + BN * 4 == NS * BN * 4 ? 0 : bias + BN * 4;
-    // all waves are done with the place of the results
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    copy_next();
+    bias = bias == NS * BN * 4 ? 0 : bias + BN * 4;
   }
 }
 
