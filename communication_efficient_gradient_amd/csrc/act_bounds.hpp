@@ -52,4 +52,25 @@ constexpr int group_lanes(int group, int64_t pitch) {
   return group / 8 < row ? group / 8 : row;
 }
 
+// Rows of several ranges are summed in steps of 64, a range of more than `most`
+// steps in parts of up to `most`.  What a grid and a workspace have to hold for
+// any ranges that lie one after the other within `rows` rows.
+struct UnitBounds {
+  int64_t steps;    // of all ranges: each may end inside one
+  int64_t split;    // ranges that have parts
+  int64_t parts;
+  int64_t units;    // parts, and ranges without
+
+  static constexpr int64_t steps_of(int64_t rows, int64_t ranges) {
+    return rows / 64 + (ranges < rows ? ranges : rows);
+  }
+
+  // a range of n > most steps has at most n / most + 1 parts
+  constexpr UnitBounds(int64_t rows, int64_t ranges, int64_t most)
+      : steps(steps_of(rows, ranges)),
+        split(steps / (most + 1) < ranges ? steps / (most + 1) : ranges),
+        parts(split > 0 ? steps / most + split : 0),
+        units(ranges + parts) {}
+};
+
 }  // namespace gq

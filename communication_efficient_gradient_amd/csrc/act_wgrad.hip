@@ -26,6 +26,36 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_act_wgrad(Wgr
                                                            a.rows, dw, w_part, db, b_part);
 }
 
+// Adds the parts of dw (splits of them) and db (splits * turns), in order:
+// four neighbouring results per thread, the loads of eight parts at a time
+// (whole quads: parts are padded to them and a quad never straddles dw's end).
+__global__ __launch_bounds__(256) void k_act_wgrad_join(WgradArgs a) {
+  const int64_t n = a.splits > 1 ? (int64_t)a.out * a.cols : 0;
+  const int64_t qw = (n + 3) / 4, total = qw + (a.db ? (a.out + 3) / 4 : 0);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const bool w = i < qw;
+    const int64_t e = (w ? i : i - qw) * 4, len = w ? n : a.out;
+    const float* q = (w ? a.ws_w : a.ws_b) + e;
+    const int64_t stride = quads(len);
+    const int parts = w ? a.splits : a.splits * a.turns;
+    f32x4 s = *(const f32x4*)q;
+    int k = 1;
+    for (; k + 8 <= parts; k += 8) {
+      f32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = *(const f32x4*)(q + (k + u) * stride);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
+    for (; k < parts; ++k) s += *(const f32x4*)(q + k * stride);
+    float* o = (w ? a.dw : a.db) + e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (e + j < len) o[j] = a.beta == 0.f ? s[j] : fmaf(a.beta, o[j], s[j]);
+  }
+}
+
 struct Plan {
   int tile, splits, otiles, ctiles, turns;
   int64_t per;
@@ -100,7 +130,7 @@ int launch_act_wgrad(const ActDims& A, int64_t out, const void* dy, int64_t lddy
                        dy,     lddy,     rows_with_room(A.rows, lddy, 7),
                        codes,  steps,    beta,        dw,           db,
                        w,      w + wn,   p.splits,    p.otiles,     p.ctiles,
-                       p.turns, p.per, out * A.cols, out};
+                       p.turns, p.per};
   // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
   const bool copy = A.dtype != GQ_F32 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
                     lddy < (1 << 23) &&

@@ -185,10 +185,9 @@ struct Plan {
 // batches: 187 us with units of 86 steps, 237 with any; 2048 tokens 69 / 65 / 61
 // us with 16 / 32 / any).
 Plan plan_wgrad(const ActDims& A, int64_t out, int experts) {
-  // steps of all experts together, at most: each may end inside one
   const int64_t rows = A.rows > 0 ? A.rows : 1;
-  const int64_t some = experts < rows ? experts : rows;
-  const int64_t steps = rows / 64 + some;
+  const int64_t some = experts < rows ? experts : rows;   // that have tokens
+  const int64_t steps = UnitBounds::steps_of(rows, experts);
   auto share = [&](double times) {
     return times < (double)some ? times * (double)steps / (double)some : (double)steps;
   };
@@ -236,12 +235,10 @@ Plan plan_wgrad(const ActDims& A, int64_t out, int experts) {
     if (m > 32.)
       consider(tile, ot, ct, (int64_t)m, 4.0 + time(cu, large < m ? large : m, (double)some, 0.));
   }
-  // an expert of n > most steps has ceil(n / most) <= 2 n / (most + 1) parts;
-  // all steps of those experts together are `steps` at most
-  const int64_t all = steps / (best.most + 1);
-  best.split_experts = all < experts ? all : experts;
-  best.parts = best.split_experts > 0 ? steps / best.most + best.split_experts : 0;
-  best.units = experts + best.parts;
+  const UnitBounds u(rows, experts, best.most);
+  best.split_experts = u.split;
+  best.parts = u.parts;
+  best.units = u.units;
   return best;
 }
 
@@ -266,11 +263,11 @@ int launch_fp8_wgrad(const ActDims& A, int64_t out, int experts, const int64_t* 
                      float beta, float* dw, float* db, void* ws, hipStream_t st) {
   const Plan p = plan_wgrad(A, out, experts);
   float* w = (float*)ws;
-  WgradArgs a = {A.rows, (int)out, (int)A.cols, (int)A.pitch, A.groups, 7,
-                       dy,     lddy,     rows_with_room(A.rows, lddy, 7),
-                       (const int8_t*)codes, steps, beta, dw, db,
-                       w,      w + p.parts * quads(out * A.cols), 1, p.otiles, p.ctiles,
-                       1,      0,        0,        0};
+  WgradArgs a = {A.rows,   (int)out, (int)A.cols, (int)A.pitch, A.groups, 7,
+                 dy,       lddy,     rows_with_room(A.rows, lddy, 7),
+                 (const int8_t*)codes, steps, beta, dw, db,
+                 w,        w + p.parts * quads(out * A.cols),
+                 1,        p.otiles, p.ctiles,    1,            0};
   const int tiles = p.otiles * p.ctiles;
   const ExpertArgs x = {experts, offsets, p.most, tiles >= 32 ? div_up(tiles, 8) : 0,
                         p.parts};

@@ -1,5 +1,5 @@
-// wgrad_tile.hpp — a tile of a linear layer's weight gradient whose input is
-// kept in an 8-bit form, and the join of its splits:
+// wgrad_tile.hpp — a tile of the weight gradient of a linear layer whose input is
+// kept in an 8-bit form:
 //   dw[o, c] <- beta dw[o, c] + sum_t dy[t, o] x^[t, c]
 //   db[o]    <- beta db[o]    + sum_t dy[t, o]
 //
@@ -43,11 +43,10 @@ struct WgradArgs {
   const float* steps;
   float beta;
   float *dw, *db;      // results
-  float *ws_w, *ws_b;  // parts: [split][all_w], [split][turns][all_b], in quads
+  float *ws_w, *ws_b;  // parts: [split][out * cols], [split][turns][out], in quads
   int splits, otiles, ctiles;
   int turns;           // tiles of a row that share the bias's sums
   int64_t per;         // tokens of a split, a multiple of 64
-  int64_t all_w, all_b;  // results: out * cols and out, of all weights together
 };
 
 // Bytes of LDS that a tile takes: two steps of dy (in each of its terms) and x^.
@@ -437,36 +436,6 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a, char* lds, int ot
       float* q = db + o0 + o;
       *q = b_part || a.beta == 0.f ? s : fmaf(a.beta, *q, s);
     }
-  }
-}
-
-// Adds the parts of dw (splits of them) and db (splits * turns), in order:
-// four neighbouring results per thread, the loads of eight parts at a time
-// (whole quads: parts are padded to them and a quad never straddles dw's end).
-__global__ __launch_bounds__(256) void k_act_wgrad_join(WgradArgs a) {
-  const int64_t n = a.splits > 1 ? a.all_w : 0;
-  const int64_t qw = (n + 3) / 4, total = qw + (a.db ? (a.all_b + 3) / 4 : 0);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const bool w = i < qw;
-    const int64_t e = (w ? i : i - qw) * 4, len = w ? n : a.all_b;
-    const float* q = (w ? a.ws_w : a.ws_b) + e;
-    const int64_t stride = quads(len);
-    const int parts = w ? a.splits : a.splits * a.turns;
-    f32x4 s = *(const f32x4*)q;
-    int k = 1;
-    for (; k + 8 <= parts; k += 8) {
-      f32x4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = *(const f32x4*)(q + (k + u) * stride);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) s += v[u];
-    }
-    for (; k < parts; ++k) s += *(const f32x4*)(q + k * stride);
-    float* o = (w ? a.dw : a.db) + e;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (e + j < len) o[j] = a.beta == 0.f ? s[j] : fmaf(a.beta, o[j], s[j]);
   }
 }
 

@@ -785,22 +785,18 @@ def _block_form(codes, steps, a: gq_act, what: str):
             _buffer(steps, torch.float32, a.rows * a.groups, what + " steps"))
 
 
-def _block_weight(form, experts: int, out: int, cols: int, what: str):
-    if form is None:
-        return None, None
-    codes, steps = form
+def _block_weight(codes, steps, experts: int, out: int, cols: int, what: str):
     blocks = -(-out // FP8_BLOCK) * -(-cols // FP8_BLOCK)
     return (_buffer(codes, E4M3, experts * out * (-(-cols // 16) * 16), what + " codes"),
             _buffer(steps, torch.float32, experts * blocks, what + " steps"))
 
 
-def _table(offsets):
-    """(pointer, experts) of an expert table; None: one expert, all rows."""
-    if offsets is None:
-        return None, 1
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets: a 1-D tensor of experts + 1 >= 2 entries")
-    return _ptr(offsets, torch.int64, "offsets"), offsets.numel() - 1
+def _table(t, what: str):
+    """(pointer, ranges) of a device table of ranges + 1 offsets."""
+    n = t.numel()
+    if n < 2 or t.dim() != 1:
+        raise ValueError(f"{what}: a 1-D tensor of at least 2 entries")
+    return _buffer(t, torch.int64, n, what), n - 1
 
 
 def gq_block_pack(a: gq_act, x: torch.Tensor, codes: torch.Tensor,
@@ -826,8 +822,12 @@ def gq_block_pack_weight(weight: gq_act, w: torch.Tensor, form=None, t_form=None
                          f"got {tuple(w.shape)}")
     experts = w.shape[0] if w.dim() == 3 else 1
     pw = _buffer(w, weight.torch_dtype, 0, "w")
-    pc, ps = _block_weight(form, experts, weight.rows, weight.cols, "weight")
-    tc, ts = _block_weight(t_form, experts, weight.cols, weight.rows, "transposed weight")
+    pc = ps = tc = ts = None
+    if form is not None:
+        pc, ps = _block_weight(*form, experts, weight.rows, weight.cols, "weight")
+    if t_form is not None:
+        tc, ts = _block_weight(*t_form, experts, weight.cols, weight.rows,
+                               "transposed weight")
     _check(_lib.gq_block_pack_weight(weight, experts, pw, pc, ps, tc, ts,
                                    _queue(stream, w)), "gq_block_pack_weight")
 
@@ -850,10 +850,10 @@ def gq_block_linear(a: gq_act, codes: torch.Tensor, steps: torch.Tensor,
     if y.dim() != 2:
         raise ValueError("y: expected a matrix")
     out = y.shape[1]
-    po, experts = _table(offsets)
+    po, experts = (None, 1) if offsets is None else _table(offsets, "offsets")
     py, ld = _matrix(y, a, out, "y")
     pc, ps = _block_form(codes, steps, a, "x")
-    wc, ws = _block_weight((w_codes, w_steps), experts, out, a.cols, "weight")
+    wc, ws = _block_weight(w_codes, w_steps, experts, out, a.cols, "weight")
     pw, nw = _space(workspace)
     _check(_lib.gq_block_linear(a, out, experts, po, pc, ps, wc, ws,
                               _vec(bias, experts * out, "bias"), py, ld, pw, nw,
@@ -878,7 +878,7 @@ def gq_block_wgrad(a: gq_act, dy: torch.Tensor, codes: torch.Tensor,
     if dy.dim() != 2:
         raise ValueError("dy: expected a matrix")
     out = dy.shape[1]
-    po, experts = _table(offsets)
+    po, experts = (None, 1) if offsets is None else _table(offsets, "offsets")
     pd, ld = _matrix(dy, a, out, "dy")
     pc, ps = _block_form(codes, steps, a, "x")
     pw, nw = _space(workspace)
@@ -937,11 +937,7 @@ def gq_adamw(d: gq_adamw_desc, g: torch.Tensor, p: torch.Tensor, m, v, step: int
     n = p.numel()
     if g.numel() != n:
         raise ValueError("g must have p's size")
-    nl = 1
-    if layer_offsets is not None:
-        po, nl = _offsets(layer_offsets), layer_offsets.numel() - 1
-    else:
-        po = None
+    po, nl = (None, 1) if layer_offsets is None else _table(layer_offsets, "layer_offsets")
     pm, sm = _state(m, d.bits, E4M3, n, "m")
     pv, sv = _state(v, d.bits, E5M2, n, "v")
     ph, kind = None, 0
