@@ -14,7 +14,10 @@
 //
 // One pass over HBM: 28 bytes per value with fp32 states, 16.1 with 8-bit ones.
 // A wave owns a block of 256 values, four to a lane, so a step needs only lane
-// exchanges.
+// exchanges.  64 M values: 328 us with fp32 states, 5.5 TB/s; 203 us with 8-bit
+// ones, 5.1 TB/s (a large copy: 5.05; the random numbers, the codes and IEEE
+// division and root fit under the loads).  25.6 M values, clipped: norm 34 us
+// under the profiler, its join 5, update 123; 160 in a loop.
 #include <type_traits>
 
 #include "adamw.hpp"

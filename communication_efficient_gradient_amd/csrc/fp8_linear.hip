@@ -13,6 +13,14 @@
 // reason why fp32 results do not take this way: there codes are decoded to
 // bf16 (exact, with their step) between LDS and the matrix instruction, whose
 // products are exact and summed in fp32, at half the rate.
+//
+// 8192 x 8192 x 4096 (tokens x out x cols): bf16 219 to 230 us in a loop, 2.4 to
+// 2.5 PFLOP/s (the library's product of the same codes with one scale for all:
+// 180 us), fp32 405 to 420 us; 16384 x 2048 x 2048 64 us, over 32 experts of 512
+// tokens 68; one token through 4096 x 4096 6.5 us, 2.6 TB/s of weight, through
+// 16384 x 8192 22.5 us, 5.9 TB/s.  Matrix cores are busy 56 % of 464k cycles at 2.1
+// GHz.  What is waited for are the copies to LDS: without any 178 us, all from
+// the same lines in L2 219 of 228, without the reads from LDS no less.
 #include <type_traits>
 
 #include "fp8.hpp"
@@ -221,11 +229,12 @@ __device__ __forceinline__ f32x4 product(i32x8 a, i32x8 b, f32x4 c, uint32_t sa,
 // 128 codes, which is one step.  An LDS row is 128 bytes in eight 16-byte
 // chunks, chunk j of row r at place j ^ (r / 2 % 8): sixteen lanes that read
 // one chunk of sixteen rows then touch every bank once.  NS k-tiles share LDS:
-// one is multiplied while NS - 1 are on their way.  Steps come for four k-tiles
-// at once, since each row's lie in a line of their own (a fetch per k-tile
-// makes half as many requests again as the codes do).  Workgroups stay and walk the tiles, and the copies
-// run on into the next tile while the present one's last products run and its
-// results leave.
+// one is multiplied while NS - 1 are on their way.  (Four halves of 64 codes
+// instead of two k-tiles, half a k-tile further ahead: 239 us instead of 219 for
+// 8192 x 8192 x 4096.)  Steps come for four k-tiles at once, since each row's lie
+// in a line of their own.  Workgroups stay and walk the tiles, and the copies run
+// on into the next tile while the present one's last products run and its results
+// leave.
 template <typename T, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(LinearArgs a) {
   constexpr bool EXACT = std::is_same_v<T, float>;

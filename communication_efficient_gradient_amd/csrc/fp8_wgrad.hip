@@ -3,6 +3,13 @@
 // and its exactness: wgrad_tile.hpp):
 //   dw[e, o, c] <- beta dw[e, o, c] + sum_{t of e} dy[t, o] x^[t, c]
 //   db[e, o]    <- beta db[e, o]    + sum_{t of e} dy[t, o]
+//
+// The sum runs over tokens, whose steps differ, so the 8-bit matrix
+// instructions cannot scale it: codes are decoded to 16 bits on their way into
+// LDS (exact).  bf16, 16384 tokens: one weight of 4096 x 4096 430 to 460 us, 1.2
+// PFLOP/s; eight of 2048 x 2048 with 2048 tokens each 155 us, with 84 to 6400 160,
+// 0.86 PFLOP/s: of a tile's 32 steps of 1.7 us and 17 us besides, its 256 KB of
+// results and the next one's first copies are what nothing runs beside.
 #include <cmath>
 
 #include "fp8.hpp"
@@ -22,6 +29,7 @@ struct ExpertArgs {
   const int64_t* offsets;
   int most;       // steps of 64 tokens that one workgroup takes
   int share;      // tiles of an XCD of each unit; 0: tiles go round the XCDs
+  int high;       // of a block of tiles that an XCD takes
   int64_t parts;  // that the workspace holds: enough for ascending tables
 };
 
@@ -120,8 +128,9 @@ __global__ __launch_bounds__((BO / WO) * (BC / WC) * 64, 2) void k_fp8_wgrad(Wgr
   }
   Unit unit;
   if (!find_unit<false>(x, a.rows, u, &unit)) return;
-  const int i8 = t / (8 * a.ctiles) * 8, h = min(8, a.otiles - i8), in = t - i8 * a.ctiles;
-  const int ot = i8 + in % h, ct = in / h;
+  // columns of `high` tiles, so that those of an XCD are a block of them
+  const int top = t / (x.high * a.ctiles) * x.high, h = min(x.high, a.otiles - top);
+  const int in = t - top * a.ctiles, ot = top + in % h, ct = in / h;
   const Tokens r = tokens_of(x.offsets, unit.expert, a.rows);
   const int64_t per = ((r.hi - r.lo + 63) / 64 + unit.splits - 1) / unit.splits * 64;
   const int64_t t0 = min(r.lo + unit.split * per, r.hi), t1 = min(t0 + per, r.hi);
@@ -268,9 +277,14 @@ int launch_fp8_wgrad(const ActDims& A, int64_t out, int experts, const int64_t* 
                  (const int8_t*)codes, steps, beta, dw, db,
                  w,        w + p.parts * quads(out * A.cols),
                  1,        p.otiles, p.ctiles,    1,            0};
-  const int tiles = p.otiles * p.ctiles;
-  const ExpertArgs x = {experts, offsets, p.most, tiles >= 32 ? div_up(tiles, 8) : 0,
-                        p.parts};
+  // What an XCD reads through its L2 is the dy of its tiles' rows and the codes
+  // of their columns: a block twice as wide as high has as many bytes of both
+  // in 16 bits (16384 tokens over 8 x 2048 x 2048, an XCD's 8 tiles of a unit 8 x 1 /
+  // 2 x 4: 582 / 279 MB fetched, 164 / 159 us; 8192 over 1024 x 1024 42 / 39 us).
+  const int tiles = p.otiles * p.ctiles, share = tiles >= 32 ? div_up(tiles, 8) : 0;
+  int high = 1;
+  while (high < 8 && 8 * high * high <= share) high *= 2;
+  const ExpertArgs x = {experts, offsets, p.most, share, high, p.parts};
   // copies move 16 bytes of a row at 16-byte addresses, to the row's last one
   const bool copy = A.dtype != GQ_F32 && ((uintptr_t)dy & 15) == 0 && lddy % 8 == 0 &&
                     lddy < (1 << 23) && out % 8 == 0;
