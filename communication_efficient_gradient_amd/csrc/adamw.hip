@@ -28,13 +28,16 @@ namespace {
 
 // An 8-bit float whose code is the upper bits of a fp32 number, `BIAS` below
 // its exponent: z = y 2^(BIAS - 127) has the code's bits from bit 23 - MAN up,
-// and what lies below is the place between two codes.
+// and what lies below is the place between two codes.  MOST: the largest code;
+// CAP: the largest step, as a biased exponent, with which it is a finite number.
 struct E4M3 {
   static constexpr int MAN = 3, TOP = 8;
+  static constexpr uint32_t MOST = 0x7e, CAP = 119 + 127;
   static constexpr float DOWN = 0x1p-120f, UP = 0x1p120f;
 };
 struct E5M2 {
   static constexpr int MAN = 2, TOP = 15;
+  static constexpr uint32_t MOST = 0x7b, CAP = 112 + 127;
   static constexpr float DOWN = 0x1p-112f, UP = 0x1p112f;
 };
 
@@ -44,11 +47,11 @@ __device__ __forceinline__ float state_value(uint32_t code, float step) {
   return __uint_as_float(bits) * F::UP * step;
 }
 
-// r16: sixteen random bits.
+// r16: sixteen random bits.  Saturates, which only a step of CAP leaves to do.
 template <typename F>
 __device__ __forceinline__ uint32_t state_code(float x, const Step& s, uint32_t r16) {
   const float z = fabsf(x) * s.inv * F::DOWN;
-  return (__float_as_uint(z) + (r16 << (7 - F::MAN))) >> (23 - F::MAN);
+  return min((__float_as_uint(z) + (r16 << (7 - F::MAN))) >> (23 - F::MAN), F::MOST);
 }
 
 struct Layer {
@@ -78,7 +81,7 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a, int64_t blocks, int6
   if (a.offsets) {
     int hi = a.layers;
     while (hi - layer > 1) {
-      const int mid = (layer + hi) / 2;
+      const int mid = layer + (hi - layer) / 2;
       if (a.offsets[mid] <= at * kStateBlock) layer = mid;
       else hi = mid;
     }
@@ -190,8 +193,8 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwArgs a, int64_t blocks, int6
           mm = max(mm, abs_bits(m[j]));
           vm = max(vm, abs_bits(v[j]));
         }
-      const Step ms = float_step<E4M3::TOP>(lanes_max(mm, 64), 119 + 127);
-      const Step vs = float_step<E5M2::TOP>(lanes_max(vm, 64), 119 + 127);
+      const Step ms = float_step<E4M3::TOP>(lanes_max(mm, 64), E4M3::CAP);
+      const Step vs = float_step<E5M2::TOP>(lanes_max(vm, 64), E5M2::CAP);
       const uint64_t q = (uint64_t)i0 / 4;
       const uint4 w = philox4x32_10(a.key0, a.key1, (uint32_t)q, (uint32_t)(q >> 32), step, 0);
       const uint32_t r[4] = {w.x, w.y, w.z, w.w};

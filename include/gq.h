@@ -545,7 +545,8 @@ int gq_block_wgrad(const gq_act* act, int64_t out, int32_t experts,
  * bits = 8: m e4m3 [n], v e5m2 [n] (OCP codes, v's sign is 0), each with fp32
  * steps [ceil(n / 256)], one per 256 consecutive elements (whatever the
  * layers): the smallest power of two with 448 * step >= the block's largest |m|
- * (57344 for v), as in the form above.  Codes are rounded at random, so that
+ * (57344 for v), from 2^-126 to 2^119 (2^112 for v), where codes saturate and
+ * states stay finite; 0 and NaN as above.  Codes are rounded at random, so that
  * the averages stay right in the mean: with f the place of the value between
  * two neighbouring codes, cut to 16 bits, up iff f + u >= 1, u from Philox4x32-10
  * with key = seed and counter = (i / 4, step); of word i mod 4 the upper 16 bits

@@ -150,8 +150,9 @@ def state_codes(x, r16, table, top: float):
     """Codes and steps of a state (float64 [n], uint64 r16 [n]); up where the
     place between two codes, cut to 16 bits, and r16 reach one."""
     n = x.size
+    cap = 112 if table is E5M2 else 119     # top * 2^cap is finite in 32 bits
     steps = np.array([step(np.abs(x[a:a + STATES]).max() if np.isfinite(x[a:a + STATES]).all()
-                           else np.nan, top) for a in range(0, n, STATES)], np.float32)
+                           else np.nan, top, cap) for a in range(0, n, STATES)], np.float32)
     s = np.repeat(steps.astype(np.float64), STATES)[:n]
     fine = s > 0
     y = np.where(fine, np.abs(x) / np.where(fine, s, 1.0), 0.0)

@@ -253,3 +253,20 @@ def test_layer_tables_out_of_range_stay_in_bounds(gq):
                         layer_offsets=dev(np.array(offsets, np.int64)),
                         decay=torch.zeros(4, device="cuda"))
     torch.cuda.synchronize()
+
+
+def test_states_near_the_largest_number_stay_finite(gq):
+    """v of 3.2e38, over the 1.75 * 2^127 that its largest step stores: saturated,
+    and the next step finds numbers."""
+    n = 512
+    d = gq.adamw(1e-3, 0.0, 0.999, 1e-8, 0.0, 8)
+
+    def gradient(t):
+        g = np.zeros(n, np.float32)
+        if t == 1:
+            g[:300] = np.sqrt(3.2e38 / np.float64(np.float32(1 - d.beta2)))
+        return g
+
+    P, (m, v) = steps_of(gq, 8, n, 3, hyper=dict(lr=1e-3, beta1=0.0, beta2=0.999, eps=1e-8),
+                         wd=0.0, gradient=gradient)
+    assert bool(torch.isfinite(P).all()) and bool(torch.isfinite(v[1]).all())

@@ -133,3 +133,10 @@ def test_state_codes_round_at_random():
     x = np.concatenate([[57344.0, 1e-30, 0.0], np.zeros(253)])
     c, s = S.state_codes(x, np.zeros(256, np.uint64), S.E5M2, 57344.0)
     assert c[:3].tolist() == [0x7b, 1, 0]
+
+
+def test_states_near_the_largest_number_stay_finite():
+    for table, top in ((S.E4M3, 448.0), (S.E5M2, 57344.0)):
+        x = np.full(256, np.float64(np.float32(3.2e38)))
+        c, s = S.state_codes(x, np.full(256, 65535, np.uint64), table, top)
+        assert np.isfinite(S.state_values(c, s, table).astype(np.float32)).all()
