@@ -70,7 +70,8 @@ bool weight_form(const uint8_t* codes, const float* steps) {
 }
 
 int check_adamw(const gq_adamw_desc* d) {
-  if (!d || !std::isfinite(d->lr) || !std::isfinite(d->weight_decay)) return GQ_EINVAL;
+  if (!d || !std::isfinite((float)d->lr) || !std::isfinite((float)d->weight_decay))
+    return GQ_EINVAL;
   if (!(d->beta1 >= 0. && d->beta1 < 1.) || !(d->beta2 >= 0. && d->beta2 < 1.)) return GQ_EINVAL;
   if (!((float)d->eps > 0.f) || !std::isfinite((float)d->eps)) return GQ_EINVAL;
   return d->bits == 32 || d->bits == 8 ? GQ_OK : GQ_EUNSUPPORTED;

@@ -563,9 +563,9 @@ int gq_block_wgrad(const gq_act* act, int64_t out, int32_t experts,
  * receives p in 16 bits (p16_dtype GQ_BF16 or GQ_F16).  Arrays that are written
  * overlap no other. */
 typedef struct {
-  double lr, beta1, beta2; /* finite; 0 <= beta < 1                          */
-  double eps;              /* > 0 as an fp32 value                           */
-  double weight_decay;     /* finite                                         */
+  double lr, beta1, beta2; /* lr finite as an fp32 value; 0 <= beta < 1      */
+  double eps;              /* finite and > 0 as an fp32 value                */
+  double weight_decay;     /* finite as an fp32 value                        */
   int32_t bits;            /* of a state's value: 32 or 8                    */
 } gq_adamw_desc;
 

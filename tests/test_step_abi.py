@@ -250,3 +250,15 @@ def test_binding_checks(gq):
         gq.gq_adamw(gq.adamw(1e-3), torch.zeros(3), torch.zeros(4), None, None, 1)
     w = gq.adamw_schedule(gq.adamw(0.5, 0.9, 0.99), 2 ** 32 - 1, lr=0.25)
     assert w.tolist()[:3] == [0.25, 1.0, 1.0] and w.view(torch.int32)[3] == -1
+
+
+def test_adamw_rates_are_finite_in_32_bits(gq):
+    L = gq.lib()
+
+    def call(**kw):
+        return L.gq_adamw(gq.adamw(**{"lr": 1e-3, **kw}), 1000, 1, None, None, None, M, None, 1,
+                          None, 2 * M, 3 * M, None, 4 * M, None, None, 0, 0, None)
+
+    for value in (1e39, -1e39, float("inf")):
+        assert call(lr=value) == -1
+        assert call(weight_decay=value) == -1
