@@ -235,13 +235,22 @@ __device__ __forceinline__ f32x4 product(i32x8 a, i32x8 b, f32x4 c, uint32_t sa,
 // in a line of their own.  Workgroups stay and walk the tiles, and the copies run
 // on into the next tile while the present one's last products run and its results
 // leave.
-template <typename T, int BM, int BN, int WM, int WN, int NS>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(LinearArgs a) {
+//
+// A small tile alone on its CU is a chain of waits (a k-tile of 64 x 64 takes 790
+// cycles, of which its products are 128; with eight k-tiles on their way instead
+// of four 18.9 us instead of 16.0 for 203 x 2050 x 4100 fp16).  TEAMS = 2: two
+// teams of waves take every second k-tile each, in step, and add up in LDS (13.3
+// us; four teams of two 12.9, but 256 x 2048 x 2048 9.0 and not 8.4).  Such a
+// workgroup takes one tile only.
+template <typename T, int BM, int BN, int WM, int WN, int NS, int TEAMS>
+__global__ __launch_bounds__(TEAMS * (BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(
+    LinearArgs a) {
   constexpr bool EXACT = std::is_same_v<T, float>;
   constexpr int BK = 128, CH = BK / 16, RPI = 64 / CH;
-  constexpr int WAVES = (BM / WM) * (BN / WN);
+  constexpr int WAVES = (BM / WM) * (BN / WN);    // of a team
+  static_assert(TEAMS == 1 || TEAMS == 2, "");
   constexpr int MT = WM / 32, NTL = WN / 32;
-  constexpr int BUF = (BM + BN) * BK;
+  constexpr int BUF = (BM + BN) * BK, ROUND = TEAMS * BUF;  // the teams' side by side
   // results leave in pieces of 16 bytes: a lane has UNITS of each 32 tokens
   constexpr int E = 16 / (int)sizeof(T), UNITS = WN / (2 * E), STORES = MT * UNITS;
   // steps of a tile's rows and of its (one or two) blocks of outputs; as many
@@ -251,18 +260,20 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   static_assert(BM / 64 < WAVES - 1 && BLOCKS <= 2, "waves for the weight's steps and the bias");
   // One array: with several the compiler tells them apart, and waits for all
   // copies before it reads from one that they may go to.
-  constexpr int STEPS = NS * BUF, BIAS = STEPS + NS * SLOT, TABLE = BIAS + (NS + 1) * BN * 4;
+  constexpr int STEPS = NS * ROUND, BIAS = STEPS + NS * SLOT, TABLE = BIAS + (NS + 1) * BN * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[TABLE + sizeof(Experts)];
   Experts& experts = *reinterpret_cast<Experts*>(&lds[TABLE]);
   const int lane = (int)threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int id = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int team = TEAMS == 1 ? 0 : id / WAVES, wave = TEAMS == 1 ? id : id % WAVES;
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
   read_experts<BM>(a, experts);
 
-  // copies: a wave instruction fills RPI rows of codes; every fourth k-tile one
-  // more brings the steps of 64 rows, or of the weight (the wave past those),
-  // and every tile's first the bias (the last wave).  Rows past the end lie
-  // behind the buffers' ranges and read as zeros.
+  // copies: a wave instruction fills RPI rows of codes, each team of its own
+  // k-tiles; every fourth k-tile one more of the first team brings the steps of
+  // 64 rows, or of the weight (the wave past those), and every tile's first the
+  // bias (the last wave).  Rows past the end lie behind the buffers' ranges and
+  // read as zeros.
   constexpr int CM = BM / RPI / WAVES, CN = BN / RPI / WAVES;
   const int cl = lane % CH, rl = lane / CH;
   const bool row_steps = wave < BM / 64;
@@ -285,11 +296,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
                         (int64_t)min(blocks - block, BLOCKS) * a.groups * 4);
   };
   const int k_tiles = a.groups;
-  // what is copied next: k-tile ck (up to cend) of the walk's last tile, into cat
+  // what is copied next: k-tile ck + team (up to cend) of the walk's last tile,
+  // into cat
   ExpertWalk copies(experts, a.experts, a.ntiles, a.splits);
   ExpertTile ctile;
   bool copying = copies.take<BM>(&ctile);
-  int ck = 0, cend = 0, cat = 0, csteps = 0, csat = 0, cbias = 0;
+  int ck = 0, cend = 0, cat = team * BUF, csteps = 0, csat = 0, cbias = 0;
   bool cfirst = true;
   auto enter = [&] {
     ranges_of(ctile);
@@ -299,8 +311,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   };
   auto copy_next = [&] {
     if (!copying) return;
-    const int k0 = ck * BK;
-    // chunks past the pitch (in the last, short k-tile) are zeros too
+    const int k0 = (ck + team) * BK;
+    // chunks past the pitch (in the last, short k-tile; the second team has one
+    // past the last of an odd number) are zeros too
     const int left = (a.pitch - k0) / 16;
 #pragma unroll
     for (int i = 0; i < CM; ++i) {
@@ -314,7 +327,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       copy16_to_lds(bn, c < left ? r * a.pitch + c * 16 : kPastEnd, k0,
                     (LdsPtr)&lds[cat + BM * BK + (wave * CN + i) * 1024]);
     }
-    if (ck == csteps) {
+    if (team == 0 && ck == csteps) {
       // what lies past a row's last step is not used
       if (row_steps || (wave == BM / 64 && lane < BLOCKS))
         copy16_to_lds(bs, step_at, ck * 4, (LdsPtr)&lds[STEPS + csat + step_to]);
@@ -326,9 +339,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       csteps += 4;
       csat = csat + SLOT == NS * SLOT ? 0 : csat + SLOT;
     }
-    cat = cat + BUF == NS * BUF ? 0 : cat + BUF;
-    if (++ck == cend) {
-      copying = copies.take<BM>(&ctile);
+    cat = cat + ROUND >= NS * ROUND ? team * BUF : cat + ROUND;
+    ck += TEAMS;
+    if (ck >= cend) {
+      copying = TEAMS == 1 && copies.take<BM>(&ctile);
       if (copying) enter();
     }
   };
@@ -381,13 +395,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
   auto read_steps = [&](int to) {
 #pragma unroll
     for (int j = 0; j < MT; ++j)
-      em[to][j] = *reinterpret_cast<const uint32_t*>(&lds[STEPS + sat + (wm + j * 32 + fr) * 16]);
+      em[to][j] = *reinterpret_cast<const uint32_t*>(&lds[STEPS + sat + team * 4 + (wm + j * 32 + fr) * 16]);
     en[to] = *reinterpret_cast<const uint32_t*>(
-        &lds[STEPS + sat + (BM + (BN > kFp8Block ? wn / kFp8Block : 0)) * 16]);
+        &lds[STEPS + sat + team * 4 + (BM + (BN > kFp8Block ? wn / kFp8Block : 0)) * 16]);
   };
   // on to the next k-tile's, `k` of them behind the tile's first
   auto next_steps = [&](int k) {
-    if (k & 3) sat += 4;
+    if (k & 3) sat += 4 * TEAMS;
     else sat = sat / SLOT + 1 == NS ? 0 : (sat / SLOT + 1) * SLOT;
   };
 
@@ -398,13 +412,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
 #pragma unroll
   for (int i = 0; i < NS; ++i) copy_next();
   meet(std::integral_constant<int, NS - 1>{}, !copying, false);
-  int at = 0, bias = 0;           // places of the k-tile and of the tile's bias
+  int at = team * BUF, bias = 0;           // places of the k-tile and of the tile's bias
   bool stored = false;
   read_steps(0);
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    read_m(j, 0, 0);
-    read_n(j, 0, 0, 0);
+    read_m(j, at, 0);
+    read_n(j, 0, at, 0);
   }
   for (;;) {
     const int n0 = tile.j * BN;
@@ -416,7 +430,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
       for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    for (int kt = first; kt < last; ++kt) {
+    for (int kt = first; kt < last; kt += TEAMS) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         if (kk == 1) {
@@ -430,15 +444,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
           meet(std::integral_constant<int, NS - 2>{}, !copying, stored);
           stored = false;
           copy_next();
-          at = at + BUF == NS * BUF ? 0 : at + BUF;
-          next_steps(kt + 1 == last ? 0 : kt + 1 - first);
+          at = at + ROUND >= NS * ROUND ? team * BUF : at + ROUND;
+          next_steps(kt + TEAMS >= last ? 0 : kt + TEAMS - first);
           read_steps(1);
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
 #pragma unroll
           for (int i = 0; i < NTL; ++i)
-            acc[i][j] = product<EXACT>(join16(fn[kk][i][0], fn[kk][i][1]),
+            // (of a k-tile past the last the steps are other rows')
+            if (TEAMS == 1 || kt + team < last)
+              acc[i][j] = product<EXACT>(join16(fn[kk][i][0], fn[kk][i][1]),
                                        join16(fm[j][0], fm[j][1]), acc[i][j], en[0], em[0][j]);
           read_m(j, at, 1 - kk);
           read_n(j, 1 - kk, at, 1 - kk);
@@ -448,6 +464,25 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
 #pragma unroll
       for (int j = 0; j < MT; ++j) em[0][j] = em[1][j];
       en[0] = en[1];
+    }
+    if constexpr (TEAMS == 2) {
+      // no copies are on their way, and behind this barrier no reads
+      __syncthreads();
+      f32x4* sums = reinterpret_cast<f32x4*>(&lds[0]) + wave * (NTL * MT * 4 * 64) + lane;
+#pragma unroll
+      for (int i = 0; i < NTL * MT * 4; ++i) {
+        const f32x16& c = acc[i / 4 / MT][i / 4 % MT];
+        const int q = i % 4 * 4;
+        if (team == 1) sums[i * 64] = f32x4{c[q], c[q + 1], c[q + 2], c[q + 3]};
+      }
+      __syncthreads();
+      if (team == 1) return;
+#pragma unroll
+      for (int i = 0; i < NTL * MT * 4; ++i) {
+        const f32x4 v = sums[i * 64];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i / 4 / MT][i / 4 % MT][i % 4 * 4 + r] += v[r];
+      }
     }
     // A lane holds, of one token per 32 x 32 tile, four consecutive outputs in
     // each of the tile's four quarters, the lane 32 further the next four.  In 16
@@ -520,7 +555,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void k_fp8_linear(Li
           }
       }
     }
-    if (!walk.take<BM>(&tile)) return;
+    if (TEAMS > 1 || !walk.take<BM>(&tile)) return;
     bias = bias == NS * BN * 4 ? 0 : bias + BN * 4;
   }
 }
@@ -670,13 +705,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_fp8_linear_few(LinearArgs a)
 // little beside the weight up to 4 tokens; from there on what one CU reads so
 // decides, which is compared below.  Measured (us here / there, bf16, tokens x
 // out x cols; what is compared behind it):
-//    1 x 16384 x 8192 22.5 / 26.6          4 x 4096 x 4096  6.7 / 15.3
-//   64 x 4096 x 4096 10.8 / 15.6 (32)     16 x 8192 x 8192 17.9 / 17.6 (32)
-//   17 x 8192 x 8192 20.0 / 18.0 (34)      8 x 20000 x 8192 32.9 / 31.4 (40)
-//   12 x 16384 x 8192 29.9 / 26.7 (48)    32 x 4608 x 8192 25.4 / 15.6 (64)
-// Several experts: 32 tokens over 16 x 1024 x 2048 7.5 / 11.1, 64 over 8 x 2048 x
-// 2048 9.8 / 10.8, 64 over 64 x 1024 x 1024 17.1 / 18.0, 128 over 32 x 2048 x
-// 2048 28.1 / 25.1.
+//    1 x 16384 x 8192 22.3 / 22.6          4 x 4096 x 4096  6.7 / 11.9
+//   64 x 4096 x 4096 10.8 / 12.1 (32)     16 x 8192 x 8192 17.9 / 16.6 (32)
+//   17 x 8192 x 8192 20.0 / 16.7 (34)      8 x 20000 x 8192 32.8 / 31.8 (40)
+//   12 x 16384 x 8192 29.8 / 23.0 (48)    32 x 4608 x 8192 25.5 / 14.2 (64)
+// Several experts: 32 tokens over 16 x 1024 x 2048 7.5 / 9.6, 64 over 8 x 2048 x
+// 2048 8.6 / 8.9, 64 over 64 x 1024 x 1024 15.0 / 17.7, 128 over 32 x 2048 x
+// 2048 31.1 / 22.4.
 bool few_tokens(const ActDims& A, int64_t out, int experts) {
   if (A.rows <= 4 || A.rows > 64) return A.rows <= 4;
   if (experts > 1) return true;
@@ -695,6 +730,11 @@ struct Plan {
   int tile;         // rows and columns of a tile
 };
 
+// Tile and splits by an estimate of the time in microseconds: rounds of
+// workgroups, a k-tile each, what a tile costs besides, and the parts' way through
+// memory and back.  Measured (bf16, whole call): 1024 x 4096 x 4096 26 us with
+// 128-tiles, 37 with 64, 48 with 256; 256 x 4096 x 4096 12.7 with 64; 100 x 1024 x
+// 8192 20.3 whole, 14.0 in 8; 512 x 2048 x 8192 21.5 whole, 28.6 in 2.
 Plan plan_linear(const ActDims& A, int64_t out, int experts) {
   const int kt = A.groups;
   Plan best = {1, kt, 0};
@@ -712,9 +752,9 @@ Plan plan_linear(const ActDims& A, int64_t out, int experts) {
       double t;
       if (tile == 256) t = rounds * (per * 1.6 + 12.0);
       else if (tile == 128) t = rounds * (per * 0.6 + 5.0);
-      else if (groups <= kCus) t = per * 0.33 + 4.0;
+      else if (groups <= kCus) t = per * 0.24 + 4.0;  // two teams
       else t = (double)((groups + 2 * kCus - 1) / (2 * kCus)) * (per * 0.44 + 4.0);
-      if (s > 1) t += 10.0 + 8.0 * (double)(s * A.rows) * (double)out / 2.4e6;
+      if (s > 1) t += 6.0 + 8.0 * (double)(s * A.rows) * (double)out / 2.4e6;
       if (t < least) {
         least = t;
         best = {div_up(kt, per), per, tile};
@@ -737,9 +777,10 @@ int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
   const int64_t tiles = ((A.rows + tile - 1) / tile + a.experts - 1) * a.ntiles * a.splits;
   const int64_t most = tile == 64 ? 2 * kCus : kCus;  // what the chip holds
   const unsigned g = (unsigned)(tiles < most ? tiles : most);
-  if (tile == 256) k_fp8_linear<T, 256, 256, 128, 64, 2><<<g, 512, 0, st>>>(a);
-  else if (tile == 128) k_fp8_linear<T, 128, 128, 64, 32, 4><<<g, 512, 0, st>>>(a);
-  else k_fp8_linear<T, 64, 64, 32, 32, 4><<<g, 256, 0, st>>>(a);
+  if (tile == 256) k_fp8_linear<T, 256, 256, 128, 64, 2, 1><<<g, 512, 0, st>>>(a);
+  else if (tile == 128) k_fp8_linear<T, 128, 128, 64, 32, 4, 1><<<g, 512, 0, st>>>(a);
+  else if (tiles <= kCus) k_fp8_linear<T, 64, 64, 32, 32, 4, 2><<<g, 512, 0, st>>>(a);
+  else k_fp8_linear<T, 64, 64, 32, 32, 4, 1><<<g, 256, 0, st>>>(a);
   int rc = (int)hipGetLastError();
   if (rc == 0 && a.splits > 1) {
     const int64_t b = (A.rows * a.out + 255) / 256;

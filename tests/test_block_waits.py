@@ -50,7 +50,7 @@ def test_products_wait_for_no_more_than_they_ask(tmp_path_factory):
     for in the inline assembly."""
     kernels = {n: lines for n, lines in assembly(tmp_path_factory, "fp8_linear").items()
                if re.search(r"12k_fp8_linearI", n)}
-    assert len(kernels) == 9                        # three types, three tiles
+    assert len(kernels) == 12       # three types, three tiles, the smallest by two teams
     for name, lines in kernels.items():
         products = [i for i, line in enumerate(lines) if line.startswith("v_mfma")]
         inline = False

@@ -134,8 +134,21 @@ def test_long_sums_are_split(gq):
     assert gq.gq_block_linear_workspace(a, 1000) > 0
     check(gq, 1111, 1000, 16000, "bf16", pad=3, lead=1)
     check(gq, 1100, 1001, 15001, "f32", whole=True, before=7, behind=11)
-    assert gq.gq_block_linear_workspace(a, 500, 3) > 0
     check(gq, 1111, 500, 16000, "f32", experts=3, whole=True, before=5, behind=2)
+    # parts of tiles that two teams take, of odd and even numbers of k-tiles
+    for dtype, cols in (("f32", 16000), ("bf16", 15001), ("f16", 8192), ("bf16", 9600)):
+        a = gq.act(1111, cols, {"f32": torch.float32, "f16": torch.float16}.get(
+            dtype, torch.bfloat16), 128)
+        assert gq.gq_block_linear_workspace(a, 100, 3) > 0
+        check(gq, 1111, 100, cols, dtype, experts=3, whole=True, before=5, behind=2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("cols", [1, 128, 129, 256, 300, 640, 1000, 1152])
+def test_tiles_of_two_teams(gq, dtype, cols):
+    """One to nine k-tiles, the second team's last one past the end or not."""
+    check(gq, 100, 150, cols, dtype, whole=True, pad=1, lead=1, seed=cols)
+    check(gq, 300, 64, cols, dtype, experts=5, before=2, behind=3, seed=cols)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
