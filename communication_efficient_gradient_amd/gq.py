@@ -793,6 +793,8 @@ def _block_weight(codes, steps, experts: int, out: int, cols: int, what: str):
 
 def _table(t, what: str):
     """(pointer, ranges) of a device table of ranges + 1 offsets."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
     n = t.numel()
     if n < 2 or t.dim() != 1:
         raise ValueError(f"{what}: a 1-D tensor of at least 2 entries")

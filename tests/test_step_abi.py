@@ -262,3 +262,14 @@ def test_adamw_rates_are_finite_in_32_bits(gq):
     for value in (1e39, -1e39, float("inf")):
         assert call(lr=value) == -1
         assert call(weight_decay=value) == -1
+
+
+def test_tables_are_tensors(gq):
+    a = gq.act(4, 6, torch.bfloat16, 128)
+    host = torch.zeros(4, 6, dtype=torch.bfloat16)
+    codes, steps = gq.alloc_block(a, device="cpu")
+    with pytest.raises(TypeError, match="offsets"):
+        gq.gq_block_linear(a, codes, steps, codes, steps, None, host, offsets=[0, 2, 4])
+    with pytest.raises(TypeError, match="layer_offsets"):
+        gq.gq_adamw(gq.adamw(1e-3), torch.zeros(4), torch.zeros(4), None, None, 1,
+                    layer_offsets=[0, 4])
