@@ -239,7 +239,7 @@ __device__ __forceinline__ f32x4 product(i32x8 a, i32x8 b, f32x4 c, uint32_t sa,
 // A small tile alone on its CU is a chain of waits (a k-tile of 64 x 64 takes 790
 // cycles, of which its products are 128; with eight k-tiles on their way instead
 // of four 18.9 us instead of 16.0 for 203 x 2050 x 4100 fp16).  TEAMS = 2: two
-// teams of waves take every second k-tile each, in step, and add up in LDS (13.3
+// teams of waves take every second k-tile each, in step, and add up in LDS (13.0
 // us; four teams of two 12.9, but 256 x 2048 x 2048 9.0 and not 8.4).  Such a
 // workgroup takes one tile only.
 template <typename T, int BM, int BN, int WM, int WN, int NS, int TEAMS>
