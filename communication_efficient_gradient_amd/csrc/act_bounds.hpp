@@ -8,9 +8,10 @@ namespace gq {
 
 // Of a matrix of `rows` rows with stride `ld`, how many (from the first on) let
 // `past` more values be read behind their last column without leaving the
-// matrix: those values lie in the following rows, ceil(past / ld) of them.
+// matrix: those values lie in the following rows, ceil(past / ld) of them.  None
+// where there are no rows: then the stride may be anything, 0 too.
 constexpr int64_t rows_with_room(int64_t rows, int64_t ld, int64_t past) {
-  return rows - (past + ld - 1) / ld;
+  return rows > 0 ? rows - (past + ld - 1) / ld : 0;
 }
 
 // The smallest p with 2^p >= v.
