@@ -9,8 +9,9 @@
 // twice the range, in e5m2.  A step of the average changes v by 0.1 % where
 // neighbouring codes lie 25 % apart, so rounding to the nearest code would
 // stop it; codes are rounded at random, up with the probability of the place
-// between them, which keeps the averages right in the mean.  v > 0 never
-// becomes 0, since m / eps would follow.
+// between them, which keeps the averages right in the mean, as long as the key is
+// not one that gq_quantize rounded the gradient by (its words are these).  v > 0
+// never becomes 0, since m / eps would follow.
 //
 // One pass over HBM: 28 bytes per value with fp32 states, 16.1 with 8-bit ones.
 // A wave owns a block of 256 values, four to a lane, so a step needs only lane

@@ -759,6 +759,9 @@ def gq_layer_norm_backward(a: gq_act, dy: torch.Tensor, x,
 E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
 FP8_BLOCK = 128         # columns that share a step, and rows of a weight
 STATE_BLOCK = 256       # values of an 8-bit state that share a step
+# gq_adamw's key where none is given: its random words have to be others than those
+# that gq_quantize rounded the gradient by, whose keys are a program's own choice
+ADAMW_SEED = 0x9d5c0fb1e3a27846
 
 
 def alloc_block(a: gq_act, device="cuda"):
@@ -932,10 +935,12 @@ def gq_adamw(d: gq_adamw_desc, g: torch.Tensor, p: torch.Tensor, m, v, step: int
              decay: torch.Tensor | None = None,
              grad_scale: torch.Tensor | None = None,
              schedule: torch.Tensor | None = None,
-             p16: torch.Tensor | None = None, seed: int = 0, stream=None) -> None:
+             p16: torch.Tensor | None = None, seed: int = ADAMW_SEED,
+             stream=None) -> None:
     """One AdamW step of p (in place) from the gradient g; m and v as
     alloc_adamw gives them; layer_offsets, lr_scale, decay: the layers' table,
-    learning rate factors and weight decays."""
+    learning rate factors and weight decays; seed (8-bit states): none that any
+    worker's gq_quantize of this gradient had."""
     n = p.numel()
     if g.numel() != n:
         raise ValueError("g must have p's size")

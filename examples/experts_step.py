@@ -106,6 +106,10 @@ class Trainer:
     """Sends the gradient as INT8 with error feedback and applies what comes
     back: clipped, AdamW with states in 8 bits."""
 
+    # Both draw random words by element and step, so each has a key of its own
+    # (of several workers each sends with another one, and all update with one).
+    UPDATE_SEED, SEND_SEED = 0, 1
+
     def __init__(self, block: Experts, lr: float, max_norm: float = 1.0, bits: int = 8):
         n = block.flat.numel()
         self.block, self.max_norm = block, max_norm
@@ -119,11 +123,12 @@ class Trainer:
     def update(self) -> None:
         b, n = self.block, self.block.flat.numel()
         self.step += 1
-        gq.gq_quantize(self.d, b.grad, self.e, 0, self.step, self.codes, self.meta)
+        gq.gq_quantize(self.d, b.grad, self.e, self.SEND_SEED, self.step, self.codes,
+                       self.meta)
         gq.gq_dequantize_accumulate(self.d, n, [self.codes], [self.meta], 1.0, 0.0, self.mean)
         gq.gq_grad_norm(self.mean, self.max_norm, b.norm, b.scale, workspace=b.ws)
         gq.gq_adamw(self.adamw, self.mean, b.flat, self.m, self.v, self.step, b.layers,
-                    decay=b.decay, grad_scale=b.scale)
+                    decay=b.decay, grad_scale=b.scale, seed=self.UPDATE_SEED)
         b.pack_weights()
 
 

@@ -551,7 +551,10 @@ int gq_block_wgrad(const gq_act* act, int64_t out, int32_t experts,
  * two neighbouring codes, cut to 16 bits, up iff f + u >= 1, u from Philox4x32-10
  * with key = seed and counter = (i / 4, step); of word i mod 4 the upper 16 bits
  * serve m, the lower 16 v.  v > 0 is never stored as 0.  All states start as
- * zeros (codes and steps).
+ * zeros (codes and steps).  gq_quantize draws the same words from the same key and
+ * step: seed has to be one that no gq_quantize of this gradient, of any worker,
+ * was given, or one number decides both roundings of an element and the averages
+ * are off in the mean.
  *
  * grad_scale (DEVICE, one fp32, or NULL for 1): the factor of gq_grad_norm; if
  * it is not finite the call changes nothing.  Otherwise a gradient that is not
