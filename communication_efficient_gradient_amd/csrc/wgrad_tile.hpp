@@ -11,7 +11,8 @@
 //   bf16  x^ = code * step is exact in bf16, dy is used as it is
 //   fp16  x^ is exact in fp16: a form of fp16 values has steps up to 2^9 (int8)
 //         or 2^7 (e4m3), and one whose smallest codes lie below 2^-24 comes with
-//         values that are multiples of 2^-24 and kept as they are
+//         values that are multiples of 2^-24 and kept as they are; a form that
+//         came from elsewhere is rounded to fp16 as unpacking rounds it
 //   fp32  dy is split into three bf16 terms (24 significant bits) whose sum is
 //         the value itself, one matrix product each with x^ in bf16; below
 //         2^-110 the third term is cut at bf16's last place, 2^-133
@@ -93,18 +94,12 @@ __device__ __forceinline__ f32x16 product(s16x8 a, s16x8 b, f32x16 c) {
   }
 }
 
-// Eight values x^ in the products' type (exact in it, see above).
+// Eight values x^ in the products' type: rounded to it as gq_*_unpack rounds them
+// (exact for forms of its values, see above).
 template <typename T>
 __device__ __forceinline__ u32x4 packed(const float (&f)[8]) {
-  if constexpr (std::is_same_v<T, _Float16>) {
-    u32x4 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      r[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(f[2 * j], f[2 * j + 1]));
-    return r;
-  } else {
-    return __builtin_bit_cast(u32x4, narrow<__bf16>(f));
-  }
+  return __builtin_bit_cast(
+      u32x4, narrow<std::conditional_t<std::is_same_v<T, float>, __bf16, T>>(f));
 }
 
 // A tile of BO output features by BC columns per workgroup, WO by WC of it per

@@ -406,8 +406,9 @@ int gq_act_linear(const gq_act* act, int64_t out, const int8_t* codes,
  *   dbias[o]      <- beta * dbias[o]      + sum_t dy[t, o]
  * dy [rows, out] in act's type, used in full (fp32 is not rounded to bf16, but
  * kept to multiples of 2^-133, which is exact from 2^-110 on, and an infinity in
- * it gives NaN); products are exact for forms that gq_act_pack writes from that
- * type, the sums are fp32.  dweight fp32 [out][cols], contiguous: a slice of the flat
+ * it gives NaN); x^ is rounded as gq_act_unpack rounds it (fp32: as for bf16), so
+ * products are exact for forms that gq_act_pack writes from that type; the sums
+ * are fp32.  dweight fp32 [out][cols], contiguous: a slice of the flat
  * gradient that gq_quantize takes.  dbias may be NULL. */
 int gq_act_wgrad_workspace(const gq_act* act, int64_t out, int64_t* bytes);
 int gq_act_wgrad(const gq_act* act, int64_t out, const void* dy, int64_t lddy,
@@ -496,10 +497,11 @@ int gq_block_pack_weight(const gq_act* weight, int32_t experts, const void* w,
 
 /* Linear layer, by expert:
  *   y[t, o] = sum_c x^[t, c] * w^[e(t), o, c] + bias[e(t), o]
- * fp32: products are exact, sums are fp32.  bf16, fp16: the 8-bit matrix cores
- * add eight products at a time, each cut at 2^-13 of the largest of the eight, and
- * these sums in 24 bits; the result is rounded once to act's type.  codes,
- * steps: the form of the input [rows, cols]; w_codes, w_steps: the experts'
+ * fp32: products are exact, sums are fp32; x^ and w^ count as multiples of 2^-133
+ * and are infinite past the largest number.  bf16, fp16: any x^ and w^; the 8-bit
+ * matrix cores add eight products at a time, each cut at 2^-13 of the largest of
+ * the eight, and these sums in 24 bits; the result is rounded once to act's type.
+ * codes, steps: the form of the input [rows, cols]; w_codes, w_steps: the experts'
  * forms [out, cols] (for the input's gradient: of their transposes, with dy's
  * form as input); bias fp32 [experts][out] or NULL.  y [rows, out], row stride
  * ldy; rows of no expert are left as they are.  workspace:
@@ -517,7 +519,9 @@ int gq_block_linear(const gq_act* act, int64_t out, int32_t experts,
  *   dweight[e, o, c] <- beta * dweight[e, o, c] + sum_{t of e} dy[t, o] * x^[t, c]
  *   dbias[e, o]      <- beta * dbias[e, o]      + sum_{t of e} dy[t, o]
  * dy [rows, out] in act's type, used as gq_act_wgrad uses it (fp32 in full);
- * codes, steps: the form of the layer's input.  dweight fp32 [experts][out]
+ * codes, steps: the form of the layer's input, with x^ as gq_block_unpack gives it
+ * in act's type (its own values for a form that was packed from that type; fp32:
+ * to a multiple of 2^-133, and an x^ past the largest number gives NaN).  dweight fp32 [experts][out]
  * [cols], dbias fp32 [experts][out] or NULL: slices of the flat gradient that
  * gq_quantize takes.  An expert without rows gets beta times what was there.
  * GQ_EUNSUPPORTED for more than 2^22 tiles of 128 x 128 results or 2^34 rows. */
