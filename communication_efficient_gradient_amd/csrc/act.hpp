@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "act_bounds.hpp"
 #include "common.hpp"
 
 namespace gq {
@@ -296,8 +297,6 @@ struct TileWalk {
     return true;
   }
 };
-
-constexpr int kCus = 256;  // compute units
 
 __host__ __device__ inline int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 

@@ -6,6 +6,8 @@
 
 namespace gq {
 
+constexpr int kCus = 256;  // compute units
+
 // Of a matrix of `rows` rows with stride `ld`, how many (from the first on) let
 // `past` more values be read behind their last column without leaving the
 // matrix: those values lie in the following rows, ceil(past / ld) of them.  None
@@ -51,6 +53,13 @@ struct Cover {
 constexpr int group_lanes(int group, int64_t pitch) {
   const int row = 1 << log2_up(pitch / 8 > 4 ? pitch / 8 : 4);
   return group / 8 < row ? group / 8 : row;
+}
+
+// Tiles of `tile` rows that ranges one after the other within `rows` rows have at
+// most: each range with rows in it may end inside one.
+constexpr int64_t ragged_tiles(int64_t rows, int64_t ranges, int64_t tile) {
+  const int64_t some = ranges < rows ? ranges : rows;
+  return (rows + some * (tile - 1)) / tile;
 }
 
 // Rows of several ranges are summed in steps of 64, a range of more than `most`

@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "fp8.hpp"
+#include "fp8_plan.hpp"
 
 namespace gq {
 namespace {
@@ -700,90 +701,28 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_fp8_linear_few(LinearArgs a)
   }
 }
 
-// Which of the two: each workgroup above reads the codes of its tokens (up to
-// 32) from L2 for 16 or 32 outputs, the tiled kernel once for 64.  That is
-// little beside the weight up to 4 tokens; from there on what one CU reads so
-// decides, which is compared below.  Measured (us here / there, bf16, tokens x
-// out x cols; what is compared behind it):
-//    1 x 16384 x 8192 22.3 / 22.6          4 x 4096 x 4096  6.7 / 11.9
-//   64 x 4096 x 4096 10.8 / 12.1 (32)     16 x 8192 x 8192 17.9 / 16.6 (32)
-//   17 x 8192 x 8192 20.0 / 16.7 (34)      8 x 20000 x 8192 32.8 / 31.8 (40)
-//   12 x 16384 x 8192 29.8 / 23.0 (48)    32 x 4608 x 8192 25.5 / 14.2 (64)
-// Several experts: 32 tokens over 16 x 1024 x 2048 7.5 / 9.6, 64 over 8 x 2048 x
-// 2048 8.6 / 8.9, 64 over 64 x 1024 x 1024 15.0 / 17.7, 128 over 32 x 2048 x
-// 2048 31.1 / 22.4.
-bool few_tokens(const ActDims& A, int64_t out, int experts) {
-  if (A.rows <= 4 || A.rows > 64) return A.rows <= 4;
-  if (experts > 1) return true;
-  const int groups = A.rows <= 32 ? div_up(out, 16) : 2 * div_up(out, 32);
-  return div_up(groups, kCus) * (A.rows < 32 ? A.rows : 32) <= 32;
-}
-
 template <typename T, int MT, int NT>
 void few(const LinearArgs& a, hipStream_t st) {
   const dim3 g(div_up(a.out, 16 * NT), a.experts, div_up(a.rows, 16 * MT));
   k_fp8_linear_few<T, MT, NT><<<g, kFewWaves * 64, 0, st>>>(a);
 }
 
-struct Plan {
-  int splits, per;  // of the sum, and 128-byte k-tiles of one
-  int tile;         // rows and columns of a tile
-};
-
-// Tile and splits by an estimate of the time in microseconds: rounds of
-// workgroups, a k-tile each, what a tile costs besides, and the parts' way through
-// memory and back.  Measured (bf16, whole call): 1024 x 4096 x 4096 26 us with
-// 128-tiles, 37 with 64, 48 with 256; 256 x 4096 x 4096 12.7 with 64; 100 x 1024 x
-// 8192 20.3 whole, 14.0 in 8; 512 x 2048 x 8192 21.5 whole, 28.6 in 2.
-Plan plan_linear(const ActDims& A, int64_t out, int experts) {
-  const int kt = A.groups;
-  Plan best = {1, kt, 0};
-  if (few_tokens(A, out, experts)) return best;
-  double least = 1e30;
-  // as if the tokens were spread evenly over the experts
-  const int64_t each = (A.rows + experts - 1) / experts;
-  const int64_t used = (A.rows + each - 1) / each;
-  for (int tile = 64; tile <= 256; tile *= 2) {
-    const int64_t tiles = used * ((each + tile - 1) / tile) * ((out + tile - 1) / tile);
-    for (int s = 1; s <= 8 && (s == 1 || kt / s >= 8); ++s) {
-      const int per = div_up(kt, s);
-      const int64_t groups = tiles * s;
-      const double rounds = (double)((groups + kCus - 1) / kCus);
-      double t;
-      if (tile == 256) t = rounds * (per * 1.6 + 12.0);
-      else if (tile == 128) t = rounds * (per * 0.6 + 5.0);
-      else if (groups <= kCus) t = per * 0.24 + 4.0;  // two teams
-      else t = (double)((groups + 2 * kCus - 1) / (2 * kCus)) * (per * 0.44 + 4.0);
-      if (s > 1) t += 6.0 + 8.0 * (double)(s * A.rows) * (double)out / 2.4e6;
-      if (t < least) {
-        least = t;
-        best = {div_up(kt, per), per, tile};
-      }
-    }
-  }
-  return best;
-}
-
 template <typename T>
-int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
-  if (few_tokens(A, a.out, a.experts)) {
-    if (a.experts > 1 || A.rows <= 16) few<T, 1, 1>(a, st);
-    else if (A.rows <= 32) few<T, 2, 1>(a, st);
+int linear_t(const LinearPlan& p, LinearArgs a, hipStream_t st) {
+  if (p.tile == 0) {
+    if (a.experts > 1 || a.rows <= 16) few<T, 1, 1>(a, st);
+    else if (a.rows <= 32) few<T, 2, 1>(a, st);
     else few<T, 2, 2>(a, st);
     return (int)hipGetLastError();
   }
-  a.ntiles = div_up(a.out, tile);
-  // at most: experts may each end inside a tile
-  const int64_t tiles = ((A.rows + tile - 1) / tile + a.experts - 1) * a.ntiles * a.splits;
-  const int64_t most = tile == 64 ? 2 * kCus : kCus;  // what the chip holds
-  const unsigned g = (unsigned)(tiles < most ? tiles : most);
-  if (tile == 256) k_fp8_linear<T, 256, 256, 128, 64, 2, 1><<<g, 512, 0, st>>>(a);
-  else if (tile == 128) k_fp8_linear<T, 128, 128, 64, 32, 4, 1><<<g, 512, 0, st>>>(a);
-  else if (tiles <= kCus) k_fp8_linear<T, 64, 64, 32, 32, 4, 2><<<g, 512, 0, st>>>(a);
+  const unsigned g = (unsigned)p.grid;
+  if (p.tile == 256) k_fp8_linear<T, 256, 256, 128, 64, 2, 1><<<g, 512, 0, st>>>(a);
+  else if (p.tile == 128) k_fp8_linear<T, 128, 128, 64, 32, 4, 1><<<g, 512, 0, st>>>(a);
+  else if (p.teams == 2) k_fp8_linear<T, 64, 64, 32, 32, 4, 2><<<g, 512, 0, st>>>(a);
   else k_fp8_linear<T, 64, 64, 32, 32, 4, 1><<<g, 256, 0, st>>>(a);
   int rc = (int)hipGetLastError();
   if (rc == 0 && a.splits > 1) {
-    const int64_t b = (A.rows * a.out + 255) / 256;
+    const int64_t b = (a.rows * a.out + 255) / 256;
     k_fp8_linear_join<T><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, st>>>(a);
     rc = (int)hipGetLastError();
   }
@@ -794,7 +733,7 @@ int linear_t(const ActDims& A, LinearArgs a, int tile, hipStream_t st) {
 
 int64_t fp8_linear_workspace(const ActDims& A, int64_t out, int experts) {
   if (A.rows == 0) return 0;
-  const Plan p = plan_linear(A, out, experts);
+  const LinearPlan p = plan_linear(A.rows, A.groups, out, experts);
   return p.splits > 1 ? 4 * p.splits * A.rows * out : 0;
 }
 
@@ -803,14 +742,15 @@ int launch_fp8_linear(const ActDims& A, int64_t out, int experts, const int64_t*
                       const float* w_steps, const float* bias, void* y, int64_t ldy, void* ws,
                       hipStream_t st) {
   if (A.rows == 0) return 0;
-  const Plan p = plan_linear(A, out, experts);
+  const LinearPlan p = plan_linear(A.rows, A.groups, out, experts);
   const LinearArgs a = {A.rows, (int)out, (int)A.pitch, A.groups, experts, offsets,
                         codes,  w_codes,  steps,        w_steps,  bias,    y,
-                        ldy,    (float*)ws, p.splits,   p.per,    0};
+                        ldy,    (float*)ws, p.splits,   p.per,
+                        p.tile ? div_up(out, p.tile) : 0};
   switch (A.dtype) {
-    case GQ_F32: return linear_t<float>(A, a, p.tile, st);
-    case GQ_BF16: return linear_t<__bf16>(A, a, p.tile, st);
-    default: return linear_t<_Float16>(A, a, p.tile, st);
+    case GQ_F32: return linear_t<float>(p, a, st);
+    case GQ_BF16: return linear_t<__bf16>(p, a, st);
+    default: return linear_t<_Float16>(p, a, st);
   }
 }
 
