@@ -8,23 +8,37 @@
 
 namespace gq {
 
-// Which of the two: a workgroup of k_fp8_linear_few reads the codes of its tokens (up to
-// 32) from L2 for 16 or 32 outputs, the tiled kernel once for 64.  That is
+// Which of the two: a workgroup of k_fp8_linear_few reads the codes of its tokens (up
+// to 32) from L2 for 16 or 32 outputs, the tiled kernel once for 64.  That is
 // little beside the weight up to 4 tokens; from there on what one CU reads so
-// decides, which is compared below.  Measured (us here / there, bf16, tokens x
-// out x cols; what is compared behind it):
+// decides, in rows, which is compared below: of one weight by whole rounds of
+// workgroups, of several experts, whose workgroups end at different times, all in
+// all.  Measured (us here / there, bf16, tokens x out x cols; what is compared
+// behind it):
 //    1 x 16384 x 8192 22.3 / 22.6          4 x 4096 x 4096  6.7 / 11.9
 //   64 x 4096 x 4096 10.8 / 12.1 (32)     16 x 8192 x 8192 17.9 / 16.6 (32)
 //   17 x 8192 x 8192 20.0 / 16.7 (34)      8 x 20000 x 8192 32.8 / 31.8 (40)
 //   12 x 16384 x 8192 29.8 / 23.0 (48)    32 x 4608 x 8192 25.5 / 14.2 (64)
-// Several experts: 32 tokens over 16 x 1024 x 2048 7.5 / 9.6, 64 over 8 x 2048 x
-// 2048 8.6 / 8.9, 64 over 64 x 1024 x 1024 15.0 / 17.7, 128 over 32 x 2048 x
-// 2048 31.1 / 22.4.
+// Several experts, tokens over experts x out x cols, even loads / uneven ones:
+//   64 over 2 x 2048 x 2048  6.7 8.4 / 8.9 8.9 (32)
+//   24 over 3 x 5120 x 5120  19.3 19.6 / 16.3 16.4 (30)
+//   64 over 16 x 2050 x 4100 25.8 26.9 / 34.6 34.3 (32)
+//   60 over 6 x 3000 x 1500  7.8 8.1 / 10.8 10.7 (44)
+//   48 over 4 x 4096 x 4096  17.7 19.6 / 14.8 14.8 (48)
+//   24 over 3 x 12000 x 1200 11.8 11.8 / 14.9 14.8 (70)
+//   64 over 2 x 4096 x 4096  18.8 21.1 / 13.0 13.1 (64)
+//   32 over 2 x 8192 x 8192  34.4 42.8 / 23.2 23.5 (64)
+//   64 over 64 x 4096 x 1024 78.9 50.1 / 50.6 30.7 (64)
+//   64 over 2 x 8192 x 8192  64.3 72.8 / 23.4 24.4 (128)
+// (1068 such pairs: 46 is 1.2 % over the faster one of each in the mean, 27 % at
+// most beyond the limit and 49 % below it; the kernel for few tokens always 4.7 %
+// and up to 199 %.)
 inline bool few_tokens(int64_t rows, int64_t out, int experts) {
   if (rows <= 4 || rows > 64) return rows <= 4;
-  if (experts > 1) return true;
-  const int64_t groups = rows <= 32 ? (out + 15) / 16 : 2 * ((out + 31) / 32);
-  return (groups + kCus - 1) / kCus * (rows < 32 ? rows : 32) <= 32;
+  const int64_t groups = (out + 15) / 16;
+  if (experts > 1) return groups * rows <= 46 * kCus;
+  return ((rows <= 32 ? groups : 2 * ((out + 31) / 32)) + kCus - 1) / kCus *
+             (rows < 32 ? rows : 32) <= 32;
 }
 
 struct LinearPlan {

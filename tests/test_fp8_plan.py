@@ -37,3 +37,16 @@ def test_shapes_reach_their_kernels(exe):
             tile, teams, splits, per, _ = map(int, r.stdout.split())
             got = (tile, teams, "parts" if splits > 1 else "whole", "odd" if per % 2 else "even")
             assert kernel == got, (rows, out, cols, experts)
+
+
+def test_few_tokens_of_several_experts_by_what_was_measured(exe):
+    """Tokens, k-tiles, out, experts: the kernel that measured faster by more than a
+    quarter with even and with uneven loads."""
+    few = [(32, 16, 1024, 16), (8, 32, 1024, 4), (32, 33, 2050, 2), (64, 33, 2050, 16),
+           (24, 12, 512, 48)]
+    tiled = [(64, 32, 4096, 2), (48, 64, 8192, 2), (64, 64, 4608, 2), (60, 40, 5120, 3),
+             (64, 32, 14336, 2), (64, 8, 4096, 64), (60, 10, 12000, 48)]
+    for shape in few + tiled:
+        r = subprocess.run([exe, *map(str, shape)], capture_output=True, text=True, timeout=60,
+                           check=True)
+        assert (r.stdout.split()[0] == "0") == (shape in few), shape
