@@ -630,10 +630,20 @@ def _space(t):
     return _buffer(t, torch.uint8, 0, "workspace"), t.numel()
 
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _queue(stream, ref: torch.Tensor):
-    """The raw stream: the one given, or the current one of ref's device."""
+    """The raw stream: the one given, or the current one of ref's device.  That has
+    to be the current device: kernels go there, also where the stream is its
+    device's default one, which has no device in its handle."""
+    device, current = ref.get_device(), _current_device()
+    if device != current:
+        raise ValueError(f"tensors on cuda:{device}, but the current device is "
+                         f"cuda:{current}: call it under torch.cuda.device({device})")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(ref.get_device())
+        return _raw_stream(device)
     return _stream(stream, ref)
 
 

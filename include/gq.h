@@ -38,6 +38,7 @@
  *     concurrently as long as their buffers do not overlap.
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *     Work is enqueued asynchronously; nothing synchronizes the device.
+ *     Kernels are launched on the current device: buffers and stream are its.
  *   - Argument errors are detected on the host before any launch and
  *     returned; a failed launch returns GQ_ELAUNCH.  A GPU dispatch holds
  *     fewer than 2^32 work-items, which bounds n per call for the kernels
