@@ -17,8 +17,10 @@
 // A wave owns a block of 256 values, four to a lane, so a step needs only lane
 // exchanges.  64 M values: 328 us with fp32 states, 5.5 TB/s; 203 us with 8-bit
 // ones, 5.1 TB/s (a large copy: 5.05; the random numbers, the codes and IEEE
-// division and root fit under the loads).  25.6 M values, clipped: norm 34 us
-// under the profiler, its join 5, update 123; 160 in a loop.
+// division and root fit under the loads).  25.6 M values, clipped: 160 us in a loop;
+// under the profiler the norm takes 34 there, behind an update that has written 307 MB,
+// its join 5, the update 123.  By itself the norm takes 20, 5.1 TB/s (24 in a loop,
+// with its join).
 #include <type_traits>
 
 #include "adamw.hpp"

@@ -21,10 +21,11 @@
 //
 // 8192 x 8192 x 4096 (tokens x out x cols): bf16 219 to 230 us in a loop, 2.4 to
 // 2.5 PFLOP/s (the library's product of the same codes with one scale for all:
-// 180 us), fp32 405 to 420 us; 16384 x 2048 x 2048 64 us, over 32 experts of 512
-// tokens 68; one token through 4096 x 4096 6.5 us, 2.6 TB/s of weight, through
-// 16384 x 8192 22.5 us, 5.9 TB/s.  Matrix cores are busy 56 % of 464k cycles at 2.1
-// GHz.  What is waited for are the copies to LDS: without any 178 us, all from
+// 180 us), on inputs from HBM 240 to 244, fp32 405 to 420 and 435; 16384 x 2048 x
+// 2048 64 us, over 32 experts of 512 tokens 68, from HBM 81 to 85 (fp32 133), of
+// uneven loads 103 (168); with transposed forms the same within 5 %.  One token
+// through 4096 x 4096 6.5 us, 2.6 TB/s of weight, through 16384 x 8192 22.5 us, 5.9
+// TB/s.  Matrix cores are busy 57 % of 460k cycles at 2.1 GHz.  What is waited for are the copies to LDS: without any 178 us, all from
 // the same lines in L2 219 of 228, without the reads from LDS no less.
 #include <type_traits>
 

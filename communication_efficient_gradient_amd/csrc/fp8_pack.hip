@@ -8,10 +8,11 @@
 // form of a block is the block's codes turned around, with the same step.
 //
 // At the rate of a large copy (5.05 TB/s here) from about 100 MB on:
-// activations 8192 x 4096 bf16 21 to 25 us, 4.1 to 4.8 TB/s; eight fp32 weights of
-// 4096 x 4096, both directions 151 us, 5.3 TB/s, one 131 or 124; bf16 116 us, 4.6
-// TB/s, and 4.0 TB/s where rows are not whole 16 bytes (32 x 1001 x 2050: 66 us,
-// 1008 x 2048 50).  Small ones are bounded by the latency of one load and one
+// activations 8192 x 4096 bf16 21 to 25 us, 4.1 to 4.8 TB/s, and back 21 (16384 rows
+// 38 both ways; fp32 30 and 34; 8192 x 4100 bf16 24 and 29, fp32 31 and 48); eight
+// fp32 weights of 4096 x 4096, both directions 151 us, 5.3 TB/s, one 131 or 124; bf16
+// 116 us, 4.6 TB/s, and 4.0 TB/s where rows are not whole 16 bytes (32 x 1001 x 2050:
+// 66 us, 1008 x 2048 50).  Small ones are bounded by the latency of one load and one
 // store: a weight of 4096 x 1024, one block per CU, 7.5 us of which 5 are its
 // bytes'.
 #include "act_bounds.hpp"

@@ -7,9 +7,11 @@
 // The sum runs over tokens, whose steps differ, so the 8-bit matrix
 // instructions cannot scale it: codes are decoded to 16 bits on their way into
 // LDS (exact).  bf16, 16384 tokens: one weight of 4096 x 4096 430 to 460 us, 1.2
-// PFLOP/s; eight of 2048 x 2048 with 2048 tokens each 155 us, with 84 to 6400 160,
-// 0.86 PFLOP/s: of a tile's 32 steps of 1.7 us and 17 us besides, its 256 KB of
-// results and the next one's first copies are what nothing runs beside.
+// PFLOP/s; eight of 2048 x 2048 with 2048 tokens each 155 us (167 on inputs from HBM,
+// fp16 171, fp32, three products, 363), with 84 to 6400 160, 0.86 PFLOP/s: of a
+// tile's 32 steps of 1.7 us and 17 us besides, its 256 KB of results and the next
+// one's first copies are what nothing runs beside: a workgroup takes one tile and
+// most of a CU's LDS, so the next one starts when it has left.
 #include <cmath>
 
 #include "fp8.hpp"
