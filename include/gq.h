@@ -553,13 +553,14 @@ int gq_block_wgrad(const gq_act* act, int64_t out, int32_t experts,
  * (57344 for v), from 2^-126 to 2^119 (2^112 for v), where codes saturate and
  * states stay finite; 0 and NaN as above.  Codes are rounded at random, so that
  * the averages stay right in the mean: with f the place of the value between
- * two neighbouring codes, cut to 16 bits, up iff f + u >= 1, u from Philox4x32-10
+ * two neighbouring codes, cut to 16 bits (below the smallest normal code it is first
+ * rounded to 20 bits for m, 21 for v), up iff f + u >= 1, u from Philox4x32-10
  * with key = seed and counter = (i / 4, step); of word i mod 4 the upper 16 bits
  * serve m, the lower 16 v.  v > 0 is never stored as 0.  All states start as
- * zeros (codes and steps).  gq_quantize draws the same words from the same key and
- * step: seed has to be one that no gq_quantize of this gradient, of any worker,
- * was given, or one number decides both roundings of an element and the averages
- * are off in the mean.
+ * zeros (codes and steps).  gq_quantize and its forms by layer draw the same words
+ * from the same key and step: seed has to be one that no worker quantized this
+ * gradient with, or one number decides both roundings of an element and the
+ * averages are off in the mean.
  *
  * grad_scale (DEVICE, one fp32, or NULL for 1): the factor of gq_grad_norm; if
  * it is not finite the call changes nothing.  Otherwise a gradient that is not
